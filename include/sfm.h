@@ -402,6 +402,134 @@ SFM_API int sfm_euler_update(float* z, const float* v, float dtau, long long n, 
 SFM_API int sfm_fm_solve_exact_velocity(const sfm_handle* h, const float* z0, float* z,
                                         const float* taus, int n_taus, void* stream);
 
+/*
+ * Attention in which every query has its own range of keys: packed documents,
+ * a prefix seen whole before a causal rest, causality, padding -- with capped
+ * scores and a distance bias.  The thinker's token-causal language / state pass
+ * ("Wan-Streamer" v0.2 blog, "Infra") over several sessions packed into one
+ * call is its use here; the pages give no formula for it.
+ *   s_ij = q_i . k_j / sqrt(D_h);  s = softcap tanh(s / softcap) if softcap > 0;
+ *   s -= slopes[h] |n_kv - n_q + i - j| if slopes;
+ *   o_i = sum_j softmax_j(s_ij) v_j over key_lo[i] <= j < key_hi[i]
+ * q, o: [n_q][n_heads][D_h]; k, v: [n_kv][n_kv_heads][D_h], n_heads a multiple of
+ * n_kv_heads (query head h reads key head h / (n_heads / n_kv_heads)); key_lo,
+ * key_hi: device int32 [n_q] (NULL: 0 and n_kv; values outside [0, n_kv] are cut
+ * to it); slopes: device fp32 [n_heads] or NULL.
+ *   - A query whose range is empty, or all of whose scores are -inf, gets zeros.
+ *   - Keys outside a query's range do not reach it whatever K and V hold there
+ *     (infinities and NaN included).
+ *   - bf16 (D_h = 128): P is rounded to bf16 for the product with V, sums and
+ *     statistics are fp32.  fp32 (D_h a multiple of 32, <= 128): fp32 throughout.
+ *   - slopes need n_kv >= n_q (the queries sit at the last n_q keys' positions).
+ *   - workspace: sfm_attention_masked_workspace_bytes(...) bytes, 16-byte aligned
+ *     (may be NULL when that is 0); nothing in it has to be set, and calls that
+ *     can overlap need their own.
+ */
+SFM_API size_t sfm_attention_masked_workspace_bytes(int n_q, int n_kv, int n_heads, int n_kv_heads,
+                                                    int head_dim, int dtype);
+SFM_API int sfm_attention_masked(const void* q, const void* k, const void* v, void* o, int n_q,
+                                 int n_kv, int n_heads, int n_kv_heads, int head_dim, int dtype,
+                                 const int* key_lo, const int* key_hi, float softcap,
+                                 const float* slopes, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * The ranges sfm_attention_masked takes, for packed documents.  Keys
+ * [doc_starts[d], doc_starts[d + 1]) are document d; query i sits at key
+ * n_kv - n_q + i and sees its own document: all of it, or (causal) the keys up
+ * to its own and the document's first prefixes[d].  Queries before the first
+ * document's start or behind the last one's end are padding: an empty range.
+ * doc_starts: device int32 [n_docs + 1], ascending (equal neighbours: an empty
+ * document), or NULL for one document of all keys (then n_docs is 0, or 1 with
+ * prefixes); prefixes: device int32 [n_docs] or NULL (0); key_lo, key_hi: device
+ * int32 [n_q].  One result serves every layer of a pass.
+ */
+SFM_API int sfm_attention_bounds(int n_q, int n_kv, const int* doc_starts, const int* prefixes,
+                                 int n_docs, int causal, int* key_lo, int* key_hi, void* stream);
+
+/* ---- paged K/V cache -------------------------------------------------------- */
+/*
+ * One layer's cache of many sequences over a pool of pages.  The pages state no
+ * cache layout or eviction policy ("Wan-Streamer v0.2" digest, "details
+ * missing"); the handle's ring cache (sfm_kvcache_append) keeps whole units in
+ * order, this one serves token-wise callers whose sequences grow at their own
+ * pace.
+ *   k_pages, v_pages  device [n_pages][page_size][n_kv_heads][D_h]; any page_size >= 1
+ *   table             device int32 [n_seq][max_pages]: slot t of sequence s is row
+ *                     t % page_size of page table[s][t / page_size].  Entries that no
+ *                     slot in use needs are not read.
+ *   lengths           device int32 [n_seq]: slots in use (0: an empty sequence)
+ *   positions         device int32 [n_seq][n_kv_heads][cap] or NULL: the position of the
+ *                     token in each slot (eviction moves tokens between slots)
+ *   weights           device fp32 [n_seq][n_kv_heads][cap] or NULL: the attention weight
+ *                     each slot has accumulated
+ * Types and head sizes as for sfm_attention.  Lengths and tables are read on the
+ * device, so a captured graph follows them.  A page outside [0, n_pages) is recorded
+ * as 0x301 in the standalone calls' error word (sfm_check_call_error) and its
+ * slots are left out; a length or slot that max_pages * page_size (or cap, where a
+ * call has state arrays) does not hold is recorded as 0x302 and cut (appended rows
+ * there are dropped).  Sequences may share pages that no call writes; a call that
+ * writes (append, evict) needs the pages it writes for one sequence alone.
+ * Workspaces: 16-byte aligned, nothing in them has to be set; calls that can
+ * overlap (streams, graphs) need their own.
+ */
+
+/*
+ * Writes new tokens: sequence s's rows [row_starts[s], row_starts[s + 1]) of k, v
+ * ([n_rows][n_kv_heads][D_h], K already rotated) go to its slots lengths[s] + i,
+ * their positions become pos0[s] + i (pos0 NULL: lengths[s] + i) and their weights
+ * 0.  row_starts: device int32 [n_seq + 1], ascending, or NULL: row s is sequence
+ * s's (n_rows = n_seq).  Rows outside all ranges are ignored.  lengths is the
+ * count BEFORE the call and is not changed: every layer of a pass appends at the
+ * same lengths.
+ */
+SFM_API int sfm_paged_append(const void* k, const void* v, void* k_pages, void* v_pages,
+                             const int* table, const int* lengths, const int* row_starts, int n_rows,
+                             int n_seq, int n_pages, int page_size, int max_pages, int n_kv_heads,
+                             int head_dim, int dtype, int* positions, const int* pos0, float* weights,
+                             int cap, void* stream);
+
+/*
+ * Attention of one new token per sequence over its cache: q, o [n_seq][n_heads][D_h].
+ *   s_t = q . k_t / sqrt(D_h), softcap as above;
+ *   s -= slopes[h] |p_q - p_t|, p_t = positions or t, p_q = q_positions[s] or lengths[s] - 1
+ *   o = sum_t softmax(s)_t v_t over slots t < lengths[s]   (length 0: zeros)
+ *   weights[s][h_kv][t] += sum of softmax(s)_t over the query heads of h_kv
+ * lengths counts the slots to attend to (the new token's own, once appended,
+ * included).  positions and q_positions go together and need slopes.  Any number of
+ * query heads per key head.  Results do not depend on timing (partials are joined
+ * in a fixed order).  workspace: the size for max_tokens = max_pages * page_size,
+ * or cap where that is smaller and the call has state arrays.
+ */
+SFM_API size_t sfm_paged_attention_workspace_bytes(int n_seq, int max_tokens, int n_heads,
+                                                   int n_kv_heads, int head_dim, int dtype,
+                                                   int with_weights);
+SFM_API int sfm_paged_attention(const void* q, const void* k_pages, const void* v_pages,
+                                const int* table, const int* lengths, void* o, int n_seq, int n_pages,
+                                int page_size, int max_pages, int n_heads, int n_kv_heads, int head_dim,
+                                int dtype, float softcap, const float* slopes, const int* positions,
+                                const int* q_positions, float* weights, int cap, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * Cuts every sequence longer than `keep` back to `keep` slots, for each key head on
+ * its own.  Kept are, in this order: tokens at a position below n_first or among the
+ * last n_recent positions (above the head's highest position - n_recent); then by
+ * accumulated weight, highest first (NaN last); ties by the lower slot.  The kept
+ * rows at slots >= keep move, in ascending order, into the evicted slots < keep:
+ * K, V, positions and weights; nothing else is touched, and slots >= keep hold
+ * what they held.  lengths is not changed (each layer cuts at the same lengths);
+ * the new one is min(lengths[s], keep), and pages behind it are free.
+ * SFM_EINVAL if keep < 1 or n_first + n_recent > keep.  workspace: max_tokens as for
+ * sfm_paged_attention, cap included.
+ */
+SFM_API size_t sfm_paged_evict_workspace_bytes(int n_seq, int max_tokens, int n_kv_heads, int keep);
+SFM_API int sfm_paged_evict(void* k_pages, void* v_pages, const int* table, const int* lengths,
+                            float* weights, int* positions, int cap, int n_seq, int n_pages,
+                            int page_size, int max_pages, int n_kv_heads, int head_dim, int dtype,
+                            int keep, int n_first, int n_recent, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 /* ---- measurement ------------------------------------------------------------ */
 /* Kernel classes timed by the profiler (index into the arrays below). */
 #define SFM_PROF_APPEND     0   /* K/V cache append                          */
@@ -444,8 +572,9 @@ SFM_API unsigned long long sfm_kernel_launch_count(void);
  * sfm_fm_solve*, sfm_velocity_units) returns SFM_EDEVICE without launching,
  * until sfm_clear_device_error (which synchronises the device and zeroes both).
  *
- * Standalone calls (sfm_attention*, sfm_linear) share one word per device:
- * sfm_check_call_error synchronises the current device, returns that word in
+ * Standalone calls (sfm_attention*, sfm_paged_*, sfm_linear) share one word per
+ * device (also 0x4nn: the masked attention kernel; 0x301, 0x302: the paged cache's
+ * tables and lengths): sfm_check_call_error synchronises the current device, returns that word in
  * *code and zeroes it.
  */
 SFM_API int sfm_check_device_error(const sfm_handle* h, int* code);

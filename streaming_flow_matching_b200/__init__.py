@@ -6,6 +6,8 @@ Importing this package loads libsfm.so (built in-tree by
 from . import _lib
 from ._lib import SfmError, lib  # noqa: F401
 from .performer import Performer, attention, attention_workspace_bytes, euler_update, linear  # noqa: F401
+from .paged import (attention_bounds, attention_masked, paged_append, paged_attention,  # noqa: F401
+                    paged_evict)
 
 __all__ = ["Performer", "attention", "attention_workspace_bytes", "euler_update", "linear", "SfmError",
-           "lib"]
+           "lib", "attention_bounds", "attention_masked", "paged_append", "paged_attention", "paged_evict"]

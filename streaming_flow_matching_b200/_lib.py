@@ -87,6 +87,15 @@ def _load():
         "sfm_attention": (i, [vp, vp, vp, vp, i, i, i, i, i, vp, sz, vp]),
         "sfm_attention_block_causal": (i, [vp, vp, vp, vp, i, i, i, i, i, i, vp, sz, vp]),
         "sfm_attention_noalloc": (i, [vp, vp, vp, vp, i, i, i, i, i, vp]),
+        "sfm_attention_masked_workspace_bytes": (sz, [i, i, i, i, i, i]),
+        "sfm_attention_masked": (i, [vp, vp, vp, vp, i, i, i, i, i, i, vp, vp, f, vp, vp, sz, vp]),
+        "sfm_attention_bounds": (i, [i, i, vp, vp, i, i, vp, vp, vp]),
+        "sfm_paged_append": (i, [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp, i, vp]),
+        "sfm_paged_attention_workspace_bytes": (sz, [i, i, i, i, i, i, i]),
+        "sfm_paged_attention": (i, [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, vp, vp, vp, i,
+                                    vp, sz, vp]),
+        "sfm_paged_evict_workspace_bytes": (sz, [i, i, i, i]),
+        "sfm_paged_evict": (i, [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, i, i, i, vp, sz, vp]),
         "sfm_linear": (i, [vp, vp, vp, i, i, i, i, i, vp]),
         "sfm_check_device_error": (i, [vp, C.POINTER(i)]),
         "sfm_clear_device_error": (i, [vp]),
@@ -120,6 +129,9 @@ EXPORTS = ["sfm_create", "sfm_destroy", "sfm_session_open", "sfm_session_reset",
            "sfm_fm_solve_guided_batched", "sfm_velocity_units", "sfm_set_graph_mode",
            "sfm_attention_workspace_bytes", "sfm_attention", "sfm_attention_block_causal",
            "sfm_attention_noalloc", "sfm_linear", "sfm_euler_update", "sfm_fm_solve_exact_velocity",
+           "sfm_attention_masked_workspace_bytes", "sfm_attention_masked", "sfm_attention_bounds",
+           "sfm_paged_append", "sfm_paged_attention_workspace_bytes", "sfm_paged_attention",
+           "sfm_paged_evict_workspace_bytes", "sfm_paged_evict",
            "sfm_profile_begin", "sfm_profile_end", "sfm_kernel_launch_count",
            "sfm_check_device_error", "sfm_clear_device_error", "sfm_check_call_error",
            "sfm_test_fault", "sfm_get_plan", "sfm_attention_batch_splits", "sfm_strerror",

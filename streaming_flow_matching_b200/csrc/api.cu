@@ -175,14 +175,6 @@ int make_b_map(CUtensorMap* m, const void* p, int n, int k, int block_n) {
   return make_tmap_bf16(m, p, 2, dims, strides, box);
 }
 
-// rows of [rows][H][128] bf16 (queries, or keys / values), box box_rows x 64 dims of one head
-int make_rows_map(CUtensorMap* m, const void* p, long long rows, int heads, int box_rows) {
-  const uint64_t dims[3] = {128, (uint64_t)heads, (uint64_t)rows};
-  const uint64_t strides[2] = {256, (uint64_t)heads * 256};
-  const uint32_t box[3] = {64, 1, (uint32_t)box_rows};
-  return make_tmap_bf16(m, p, 3, dims, strides, box);
-}
-
 GemmArgs gemm_args(int M, int N, int K, int epi, void* C, int ldc, const Guard& gd, int block_n,
                    bool pair) {
   GemmArgs g{};
@@ -948,8 +940,7 @@ int current_context(void** ctx) {
 }
 }  // namespace sfm
 
-namespace {
-
+namespace sfm {
 int call_guard(Guard* gd) {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
@@ -973,6 +964,9 @@ int call_guard(Guard* gd) {
   if (g_call_wait_ns) gd->wait_ns = g_call_wait_ns;
   return SFM_OK;
 }
+}  // namespace sfm
+
+namespace {
 
 // Standalone attention, every key visible (unit_tokens = 0) or block-causal over
 // query units of unit_tokens with the first n_kv - n_q keys a shared prefix.

@@ -1,0 +1,953 @@
+// Attention under per-query key ranges: packed documents, prefixes, causality and any
+// other mask that leaves each query one interval of keys, with capped scores and a
+// distance bias:
+//   s_ij = q_i . k_j / sqrt(D);  s = cap tanh(s / cap);  s -= slope_h |pos_i - j|
+//   O_i = sum_j softmax(s_i)_j v_j over j in [lo_i, hi_i);  an empty range gives zeros.
+// Groups of query heads share a key head.
+//
+// bf16 (D = 128) runs on the tensor cores (tcgen05), bound by them and by the softmax
+// beside them.  One CTA = two 128-row query tiles over the same key tiles: two heads of
+// one group at the same rows where the group is even (both tiles then have the same
+// ranges and no key tile is loaded for the sake of one of them), else 256 rows of one
+// head.  352 threads:
+//   warp 0      TMA producer: the Q tiles once, K tiles (128 keys) in a 3-stage ring, V
+//               tiles in a 2-stage ring (128-byte swizzle)
+//   warp 1      TMEM allocator; one lane issues S_t = Q_t K_j^T and O_t += P_t V_j (P from
+//               TMEM), alternating the tiles
+//   warps 2-9   softmax, thread = query row: one pass over S computes P against the
+//               running max, which moves only when a score passes it by 2^8
+//   warp 10     makes V safe: a masked key has weight 0, and 0 x inf or 0 x NaN would
+//               still reach rows that may not see it.  In key tiles that some row does not
+//               see whole it scans V and replaces non-finite elements by 0; if it found
+//               any, the rows that do see them get them added back at the end (a row's sum
+//               with a non-finite term is that term, whatever its weight).
+// The CTA's key tiles are those that the union of its rows' ranges touches (a reduction
+// over the rows' bounds at the start; nothing outside is loaded); a tile inside every
+// row's range is not masked.  The last query blocks go first in the grid: under a causal
+// mask they have the most keys.
+// Few query rows over many keys: the key tiles are cut into splits whose fp32 partials a
+// second kernel joins.
+//
+// fp32 runs on the CUDA cores in 64 x 64 tiles.
+#include <limits.h>
+#include <math.h>
+
+#include "attn_masked.cuh"
+#include "sm100.cuh"
+
+namespace sfm {
+
+using namespace sm100;
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------------ bounds
+
+// Query i of document d (starts[d] <= pos < starts[d + 1]): keys from starts[d] up to the
+// document's end, or (causal) up to max(pos + 1, starts[d] + prefix[d]).
+__global__ void __launch_bounds__(256) attention_bounds_kernel(const __grid_constant__ BoundsArgs a) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.n_q) return;
+  const int pos = a.n_kv - a.n_q + i;
+  int lo = 0, hi = 0;
+  int d = 0, start = 0, end = a.n_kv;
+  bool in = true;
+  if (a.doc_starts) {
+    in = pos >= __ldg(a.doc_starts) && pos < __ldg(a.doc_starts + a.n_docs);
+    int x = 0, y = a.n_docs;                       // the last d with starts[d] <= pos
+    while (in && y - x > 1) {
+      const int mid = (x + y) >> 1;
+      if (__ldg(a.doc_starts + mid) <= pos) x = mid;
+      else y = mid;
+    }
+    d = x;
+    if (in) {
+      start = max(0, __ldg(a.doc_starts + d));
+      end = min(a.n_kv, __ldg(a.doc_starts + d + 1));
+    }
+  }
+  if (in) {
+    lo = start;
+    hi = end;
+    if (a.causal) {
+      const long long pre = (long long)start + (a.prefixes ? max(0, __ldg(a.prefixes + d)) : 0);
+      hi = (int)min((long long)end, max((long long)pos + 1, pre));
+    }
+  }
+  a.key_lo[i] = lo;
+  a.key_hi[i] = hi;
+}
+
+// ------------------------------------------------------------------ bf16, tcgen05
+
+constexpr int BQ = 128, QT = 2, BKV = 128, D = 128;
+constexpr int THREADS = 352;
+constexpr int KST = 3, VST = 2;
+constexpr int HALF = 128 * 64 * 2;
+constexpr int TILE = 2 * HALF;
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + QT * TILE;
+constexpr int OFF_V = OFF_K + KST * TILE;
+constexpr int OFF_BAR = OFF_V + VST * TILE;
+constexpr int SMEM = OFF_BAR + 512 + 1024;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kMaxKeySplits = 16;
+constexpr int kSms = 148;
+
+struct TcArgs {
+  MaskedArgs m;
+  int paired;          // the CTA's tiles: 1 = two heads of a group, 0 = two row blocks of a head
+  int hgroups;         // heads (or pairs of heads)
+  int qblocks;         // row blocks per head group
+  int n_splits;
+  float* o_part;       // [split][n_q][H][D]
+  float* lse_part;     // [split][n_q][H] (log2)
+  int* err;
+  unsigned long long wait_ns;
+  int fault;
+};
+
+// the key range of query row i, empty as [0, 0)
+__device__ __forceinline__ void row_range(const MaskedArgs& m, int i, int* lo, int* hi) {
+  int a = m.key_lo ? max(0, __ldg(m.key_lo + i)) : 0;
+  int b = m.key_hi ? min(m.n_kv, __ldg(m.key_hi + i)) : m.n_kv;
+  if (a >= b) a = b = 0;
+  *lo = a;
+  *hi = b;
+}
+
+// keys [lo, hi) of a 32-column chunk as a bit mask (lo, hi relative to its first column)
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  if (lo >= hi) return 0u;
+  return (0xffffffffu << lo) & (0xffffffffu >> (32 - hi));
+}
+
+__device__ __forceinline__ bool nonfinite16(uint32_t w) {   // either half's exponent all ones
+  return (((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0u;
+}
+
+// tanh(x) = 1 - 2 / (2^(2 log2(e) x) + 1): absolute error a few 2^-24, which the cap scales
+__device__ __forceinline__ float tanh_ex2(float x) {
+  const float e = ex2_approx(x * (2.f * kLog2e));
+  return 1.f - __fdividef(2.f, e + 1.f);
+}
+
+// what turns a row's raw products into log2 scores
+struct ScoreMap {
+  float sc;         // scale log2(e), or scale / cap
+  float cap2;       // cap log2(e)
+  float slope2;     // slope log2(e)
+};
+
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ float score2(const ScoreMap& sm, float x, float fq, float col) {
+  float z = x * sm.sc;
+  if (CAP) z = sm.cap2 * tanh_ex2(z);
+  if (BIAS) z = fmaf(-sm.slope2, fabsf(fq - col), z);
+  return z;
+}
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_masked_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TcArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* v_full = k_empty + KST;
+  uint64_t* v_ok = v_full + VST;      // V landed and safe to multiply
+  uint64_t* v_empty = v_ok + VST;
+  uint64_t* s_full = v_empty + VST;   // [QT]
+  uint64_t* p_full = s_full + QT;     // [QT]
+  uint64_t* o_done = p_full + QT;     // [QT]
+  uint64_t* drain = o_done + QT;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* dirty = reinterpret_cast<volatile int*>(tmem_slot + 2);   // non-finite V was replaced
+  int* red = reinterpret_cast<int*>(tmem_slot + 4);                       // [4][8]
+
+  const MaskedArgs& m_ = args.m;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int rem = blockIdx.x;
+  const int hg = rem % args.hgroups;
+  rem /= args.hgroups;
+  const int split = rem % args.n_splits;
+  const int qb = args.qblocks - 1 - rem / args.n_splits;
+  const int h_a = args.paired ? 2 * hg : hg;                   // head of tile A
+  const int dh = args.paired ? 1 : 0;                          // tile B: head h_a + dh,
+  const int dr = args.paired ? 0 : BQ;                         //         rows + dr
+  const int row0 = qb * (args.paired ? BQ : 2 * BQ);
+  const int hk = h_a / (m_.heads / m_.kv_heads);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int i = 0; i < KST; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < VST; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_ok[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int t = 0; t < QT; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&o_done[t], 1);
+    }
+    mbar_init(drain, 1);
+    *abort = 0;
+    *dirty = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch(&map_q);
+    tma_prefetch(&map_k);
+    tma_prefetch(&map_v);
+  }
+  // the rows' key ranges: this thread's row (softmax warps), and over the CTA's rows the
+  // union and the intersection
+  const int st = (warp - 2) >> 2;                              // tile of a softmax warp
+  const int quarter = warp & 3;
+  const int r = quarter * 32 + lane;
+  int my_lo = 0, my_hi = m_.n_kv;
+  bool live = false;                                           // the row exists
+  if (warp >= 2 && warp < 10) {
+    const int i = row0 + st * dr + r;
+    int u_lo = INT_MAX, u_hi = 0, n_lo = 0, n_hi = INT_MAX;
+    if (i < m_.n_q) {                                          // rows past the end see all, write nothing
+      live = true;
+      row_range(m_, i, &my_lo, &my_hi);
+      if (my_hi > my_lo) {
+        u_lo = my_lo;
+        u_hi = my_hi;
+      }
+      n_lo = my_lo;
+      n_hi = my_hi;
+    }
+    u_lo = __reduce_min_sync(0xffffffffu, u_lo);
+    u_hi = __reduce_max_sync(0xffffffffu, u_hi);
+    n_lo = __reduce_max_sync(0xffffffffu, n_lo);
+    n_hi = __reduce_min_sync(0xffffffffu, n_hi);
+    if (lane == 0) {
+      red[0 * 8 + warp - 2] = u_lo;
+      red[1 * 8 + warp - 2] = u_hi;
+      red[2 * 8 + warp - 2] = n_lo;
+      red[3 * 8 + warp - 2] = n_hi;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int all_lo = INT_MAX, all_hi = 0, full_lo = 0, full_hi = INT_MAX;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    all_lo = min(all_lo, red[w]);
+    all_hi = max(all_hi, red[8 + w]);
+    full_lo = max(full_lo, red[16 + w]);
+    full_hi = min(full_hi, red[24 + w]);
+  }
+  const int u0 = all_lo < all_hi ? all_lo / BKV : 0;
+  const int u1 = all_lo < all_hi ? (all_hi + BKV - 1) / BKV : 0;
+  const int tps = (u1 - u0 + args.n_splits - 1) / args.n_splits;
+  const int t0 = min(u1, u0 + split * tps);
+  const int T = min(u1, t0 + tps) - t0;
+  // a key tile inside every row's range
+  auto whole = [&](int j) { return (t0 + j) * BKV >= full_lo && (t0 + j + 1) * BKV <= full_hi; };
+
+  if (warp == 0) {
+    if (lane == 0 && T > 0 && !(args.fault & SFM_FAULT_ATTN_NO_LOADS)) {
+      // ---------------- TMA producer ----------------
+      int kp[KST], vp[VST];
+      for (int i = 0; i < KST; ++i) kp[i] = -1;
+      for (int i = 0; i < VST; ++i) vp[i] = -1;
+      bool ok = true;
+      mbar_arrive_expect_tx(q_full, QT * TILE);
+      for (int t = 0; t < QT; ++t) {
+        tma_load_3d(base + OFF_Q + t * TILE, &map_q, q_full, 0, h_a + t * dh, row0 + t * dr);
+        tma_load_3d(base + OFF_Q + t * TILE + HALF, &map_q, q_full, 64, h_a + t * dh, row0 + t * dr);
+      }
+      auto load_k = [&](int i) -> bool {
+        const int s = i % KST;
+        const uint32_t par = (uint32_t)((i / KST) & 1);
+        if (!mbar_wait(&k_empty[s], par ^ 1u, abort, args.err, 0x401, args.wait_ns)) return false;
+        mbar_arrive_expect_tx(&k_full[s], TILE);
+        tma_load_3d(base + OFF_K + s * TILE, &map_k, &k_full[s], 0, hk, (t0 + i) * BKV);
+        tma_load_3d(base + OFF_K + s * TILE + HALF, &map_k, &k_full[s], 64, hk, (t0 + i) * BKV);
+        kp[s] = (int)par;
+        return true;
+      };
+      auto load_v = [&](int i) -> bool {
+        const int s = i % VST;
+        const uint32_t par = (uint32_t)((i / VST) & 1);
+        if (!mbar_wait(&v_empty[s], par ^ 1u, abort, args.err, 0x402, args.wait_ns)) return false;
+        mbar_arrive_expect_tx(&v_full[s], TILE);
+        tma_load_3d(base + OFF_V + s * TILE, &map_v, &v_full[s], 0, hk, (t0 + i) * BKV);
+        tma_load_3d(base + OFF_V + s * TILE + HALF, &map_v, &v_full[s], 64, hk, (t0 + i) * BKV);
+        vp[s] = (int)par;
+        return true;
+      };
+      ok = load_k(0);
+      if (ok && T > 1) ok = load_k(1);
+      for (int j = 0; j < T && ok; ++j) {
+        ok = load_v(j);
+        if (ok && j + 2 < T) ok = load_k(j + 2);
+      }
+      if (!ok) {   // unwinding: let issued loads land before the CTA exits
+        mbar_drain(q_full, 0, args.wait_ns);
+        for (int i = 0; i < KST; ++i)
+          if (kp[i] >= 0) mbar_drain(&k_full[i], (uint32_t)kp[i], args.wait_ns);
+        for (int i = 0; i < VST; ++i)
+          if (vp[i] >= 0) mbar_drain(&v_full[i], (uint32_t)vp[i], args.wait_ns);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && T > 0) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t idesc_s = idesc_bf16(BQ, BKV, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16(BQ, D, false, true);
+      bool ok = mbar_wait(q_full, 0, abort, args.err, 0x403, args.wait_ns), issued = false;
+      auto issue_s = [&](int t, int ks) {
+        const uint32_t qa = base + OFF_Q + t * TILE, ka = base + OFF_K + ks * TILE;
+        const uint32_t d = tmem + (uint32_t)(t * 256);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t sub = (uint32_t)(kk >> 2) * HALF;
+          const uint64_t da = sw128_desc(qa + sub, 16, 1024) + (uint64_t)(2 * (kk & 3));
+          const uint64_t db = sw128_desc(ka + sub, 16, 1024) + (uint64_t)(2 * (kk & 3));
+          umma_bf16(d, da, db, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[t]);
+        issued = true;
+      };
+      if (ok && (ok = mbar_wait(&k_full[0], 0, abort, args.err, 0x404, args.wait_ns))) {
+        tc_fence_after();
+        issue_s(0, 0);
+        issue_s(1, 0);
+        umma_commit(&k_empty[0]);
+      }
+      for (int j = 0; j < T && ok; ++j) {
+        const int vs = j % VST;
+        const bool more = j + 1 < T;
+        const int ks = (j + 1) % KST;
+        const uint32_t vpar = (uint32_t)((j / VST) & 1);
+        if (!mbar_wait(&v_full[vs], vpar, abort, args.err, 0x406, args.wait_ns) ||
+            !mbar_wait(&v_ok[vs], vpar, abort, args.err, 0x40C, args.wait_ns)) {
+          ok = false;
+          break;
+        }
+        const uint32_t va = base + OFF_V + vs * TILE;
+        for (int t = 0; t < QT && ok; ++t) {
+          if (!mbar_wait(&p_full[t], (uint32_t)(j & 1), abort, args.err, 0x405, args.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t pa = tmem + (uint32_t)(t * 256);
+          const uint32_t d = tmem + (uint32_t)(t * 256 + 128);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t db = sw128_desc(va + (uint32_t)kk * 2048u, HALF, 1024);
+            umma_bf16_tmem_a(d, pa + (uint32_t)(kk * 8), db, idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&o_done[t]);
+          if (t == QT - 1) umma_commit(&v_empty[vs]);
+          if (more) {
+            if (t == 0 &&
+                !mbar_wait(&k_full[ks], (uint32_t)(((j + 1) / KST) & 1), abort, args.err, 0x404, args.wait_ns)) {
+              ok = false;
+              break;
+            }
+            // S_t(j+1) overwrites P_t(j): wait until O_t's P V of this tile has completed
+            if (!mbar_wait(&o_done[t], (uint32_t)(j & 1), abort, args.err, 0x40B, args.wait_ns)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_s(t, ks);
+            if (t == QT - 1) umma_commit(&k_empty[ks]);
+          }
+        }
+      }
+      if (!ok && issued) {
+        umma_commit(drain);
+        mbar_drain(drain, 0, args.wait_ns);
+      }
+    }
+  } else if (warp == 10) {
+    // ---------------- V made safe ----------------
+    for (int j = 0; j < T; ++j) {
+      const int vs = j % VST;
+      if (!__all_sync(0xffffffffu, mbar_wait(&v_full[vs], (uint32_t)((j / VST) & 1), abort, args.err, 0x409, args.wait_ns)))
+        break;
+      if (!whole(j)) {
+        uint4* p = reinterpret_cast<uint4*>(smem + OFF_V + vs * TILE);
+        bool found = false;
+#pragma unroll 8
+        for (int i = lane; i < TILE / 16; i += 32) {
+          uint4 x = p[i];
+          if (nonfinite16(x.x) | nonfinite16(x.y) | nonfinite16(x.z) | nonfinite16(x.w)) {
+            uint32_t* w = &x.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xffff0000u;
+              if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0x0000ffffu;
+            }
+            p[i] = x;
+            found = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, found)) {
+          if (lane == 0) *dirty = 1;
+          fence_proxy_async_smem();
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_ok[vs]);
+    }
+  } else {
+    // ---------------- softmax + output (thread = query row of tile st) ----------------
+    const int t = st;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t col_s = (uint32_t)(t * 256), col_o = col_s + 128;
+    const int h = h_a + t * dh;
+    const int row_t = row0 + t * dr;                           // first row of the tile
+    const int w_lo = __reduce_max_sync(0xffffffffu, my_lo), w_hi = __reduce_min_sync(0xffffffffu, my_hi);
+    // what any row of the warp sees (an empty row, or one past the end: nothing)
+    const int any_lo = __reduce_min_sync(0xffffffffu, live && my_hi > my_lo ? my_lo : INT_MAX);
+    const int any_hi = __reduce_max_sync(0xffffffffu, live ? my_hi : 0);
+    ScoreMap sm;
+    const float scale = 0.08838834764831845f;                  // 1 / sqrt(128)
+    sm.sc = CAP ? scale / m_.softcap : scale * kLog2e;
+    sm.cap2 = m_.softcap * kLog2e;
+    sm.slope2 = BIAS ? __ldg(m_.slopes + h) * kLog2e : 0.f;
+    const int my_pos = m_.n_kv - m_.n_q + row_t + r;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < T && ok; ++j) {
+      const int key0 = (t0 + j) * BKV;
+      const bool masked = !(key0 >= w_lo && key0 + BKV <= w_hi);
+      const bool nothing = key0 >= any_hi || key0 + BKV <= any_lo;
+      const int lo = my_lo - key0, hi = my_hi - key0;
+      const float fq = (float)(my_pos - key0);
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)(j & 1), abort, args.err, 0x407, args.wait_ns))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t pk[4][16];
+      if (nothing) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[c][i] = 0u;
+      } else {
+        // P = 2^(z - m); masked columns give 0.  Returns the row's sum.
+        auto attempt = [&](float neg_m) -> float {
+          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t u[2][32];
+          tmem_ld32(tmem + lane_base + col_s, u[0]);
+          tmem_wait_ld(u[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c + 1 < 4) tmem_ld32(tmem + lane_base + col_s + (c + 1) * 32, u[(c + 1) & 1]);
+            const float* sv = reinterpret_cast<const float*>(u[c & 1]);
+            const uint32_t bits = masked ? range_bits(lo - c * 32, hi - c * 32) : 0xffffffffu;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float p[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int col = 2 * i + e;
+                float z = score2<CAP, BIAS>(sm, sv[col], fq, (float)(c * 32 + col)) + neg_m;
+                if (masked && !((bits >> col) & 1u)) z = -INFINITY;
+                p[e] = ex2_approx(z);
+                l4[col & 3] += p[e];
+              }
+              pk[c][i] = pack_bf16x2(p[0], p[1]);
+            }
+            if (c + 1 < 4) tmem_wait_ld(u[(c + 1) & 1]);
+          }
+          return (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        };
+        auto row_max = [&]() -> float {                        // of the visible scores
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[32];
+            tmem_ld32(tmem + lane_base + col_s + c * 32, w);
+            tmem_wait_ld(w);
+            const float* sv = reinterpret_cast<const float*>(w);
+            const uint32_t bits = masked ? range_bits(lo - c * 32, hi - c * 32) : 0xffffffffu;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float z = score2<CAP, BIAS>(sm, sv[i], fq, (float)(c * 32 + i));
+              if ((bits >> i) & 1u) mx = fmaxf(mx, z);
+            }
+          }
+          return mx;
+        };
+        float lt = 0.f;
+        bool again = m == -INFINITY;                           // no max yet: take it first
+        if (!__all_sync(0xffffffffu, again)) {
+          lt = attempt(m == -INFINITY ? 0.f : -m);
+          // a score can only have passed the max by 2^8 if the row's sum did
+          again = again || !(lt <= 256.f);
+        }
+        if (__any_sync(0xffffffffu, again)) {
+          const float mx = row_max();
+          const bool grown = mx > m + kRescaleLog2;            // also from m = -inf
+          if (__any_sync(0xffffffffu, grown)) {
+            const float m_new = fmaxf(m, mx);
+            const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);   // O, l are 0 then
+            l *= alpha;
+            m = m_new;
+            if (j > 0) {
+              // O_t's previous P V has completed (S_t(j) was issued after it): rescale it
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lane_base + col_o + c * 32, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st32(tmem + lane_base + col_o + c * 32, o);
+              }
+            }
+            lt = attempt(m == -INFINITY ? 0.f : -m);
+          } else if (__all_sync(0xffffffffu, m == -INFINITY)) {
+            lt = attempt(0.f);                                 // every score seen is -inf or masked
+          }
+        }
+        l += lt;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_st16(tmem + lane_base + col_s + c * 16, pk[c]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[t]);
+    }
+    // ---- output ----
+    if (ok && T > 0) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&o_done[t], (uint32_t)((T - 1) & 1), abort, args.err, 0x40A, args.wait_ns))) ok = false;
+      tc_fence_after();
+    }
+    const int q_rows = min(BQ, m_.n_q - row_t);                // may be <= 0
+    const size_t ld = (size_t)m_.heads * D;
+    const bool have = ok && T > 0 && (l > 0.f || l != l);
+    const float inv = have ? 1.f / l : 0.f;
+    if (ok) {
+      // stage the warp's 32 normalised rows in shared memory (the Q and K stages, which
+      // nothing reads any more), then write whole rows; float4 slot q of row i is at q ^ i
+      float4* stage = reinterpret_cast<float4*>(smem + OFF_Q) + (warp - 2) * (32 * 32);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t u[32];
+        if (T > 0) {
+          tmem_ld32(tmem + lane_base + col_o + c * 32, u);
+          tmem_wait_ld(u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) u[i] = 0u;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float4 f;
+          f.x = have ? __uint_as_float(u[4 * q]) * inv : 0.f;
+          f.y = have ? __uint_as_float(u[4 * q + 1]) * inv : 0.f;
+          f.z = have ? __uint_as_float(u[4 * q + 2]) * inv : 0.f;
+          f.w = have ? __uint_as_float(u[4 * q + 3]) * inv : 0.f;
+          stage[lane * 32 + ((c * 8 + q) ^ lane)] = f;
+        }
+      }
+      __syncwarp();
+      const bool fix = T > 0 && *dirty != 0;
+      for (int rr = 0; rr < 32; ++rr) {
+        if (quarter * 32 + rr >= q_rows) break;                // warp-uniform
+        float4 f = stage[rr * 32 + (lane ^ rr)];
+        if (fix) {
+          // the non-finite elements of V that this row sees, in the tiles they were taken out of
+          const int lo = __shfl_sync(0xffffffffu, my_lo, rr), hi = __shfl_sync(0xffffffffu, my_hi, rr);
+          for (int j = 0; j < T; ++j) {
+            if (whole(j)) continue;
+            const int k1 = min(hi, (t0 + j + 1) * BKV);
+            for (int k = max(lo, (t0 + j) * BKV); k < k1; ++k) {
+              const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(m_.v) +
+                                                              ((size_t)k * m_.kv_heads + hk) * D + 4 * lane);
+              if (nonfinite16(x.x) || nonfinite16(x.y)) {
+                const float v0 = __uint_as_float(x.x << 16), v1 = __uint_as_float(x.x & 0xffff0000u);
+                const float v2 = __uint_as_float(x.y << 16), v3 = __uint_as_float(x.y & 0xffff0000u);
+                if (!isfinite(v0)) f.x += v0;
+                if (!isfinite(v1)) f.y += v1;
+                if (!isfinite(v2)) f.z += v2;
+                if (!isfinite(v3)) f.w += v3;
+              }
+            }
+          }
+        }
+        const size_t at = (size_t)(row_t + quarter * 32 + rr) * ld + (size_t)h * D + 4 * lane;
+        if (args.n_splits == 1) {
+          uint2 b;
+          b.x = pack_bf16x2(f.x, f.y);
+          b.y = pack_bf16x2(f.z, f.w);
+          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(m_.o) + at) = b;
+        } else {
+          *reinterpret_cast<float4*>(args.o_part + (size_t)split * m_.n_q * ld + at) = f;
+        }
+      }
+    } else if (r < q_rows) {
+      // unwinding after a timed-out wait: zeros, written directly
+      const size_t at = (size_t)(row_t + r) * ld + (size_t)h * D;
+      if (args.n_splits == 1) {
+        uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(m_.o) + at);
+        for (int q = 0; q < D / 8; ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        float4* d = reinterpret_cast<float4*>(args.o_part + (size_t)split * m_.n_q * ld + at);
+        for (int q = 0; q < D / 4; ++q) d[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    if (r < q_rows && args.n_splits > 1)
+      args.lse_part[((size_t)split * m_.n_q + row_t + r) * m_.heads + h] = have ? m + log2f(l) : -INFINITY;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the splits of a (row, head): one warp each, 4 dims per lane.  A row no split of
+// which saw a key gets zeros.
+__global__ void __launch_bounds__(256)
+    masked_join_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_part,
+                       __nv_bfloat16* __restrict__ o, long long rows_heads, int n_splits) {
+  const long long gw = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (gw >= rows_heads) return;
+  float mx = -INFINITY;
+  for (int s = 0; s < n_splits; ++s) mx = fmaxf(mx, lse_part[s * rows_heads + gw]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  bool bad = false;                                            // some split's sum was not a number
+#pragma unroll 4
+  for (int s = 0; s < n_splits; ++s) {
+    const float ls = lse_part[s * rows_heads + gw];
+    bad |= ls != ls;
+    if (ls == -INFINITY) continue;                             // the split saw no key of this row
+    const float4 p = reinterpret_cast<const float4*>(o_part + (s * rows_heads + gw) * D)[lane];
+    const float w = exp2f(ls - mx);
+    sum += w;
+    acc.x = fmaf(w, p.x, acc.x);
+    acc.y = fmaf(w, p.y, acc.y);
+    acc.z = fmaf(w, p.z, acc.z);
+    acc.w = fmaf(w, p.w, acc.w);
+  }
+  const float inv = bad ? NAN : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+  uint2 b;
+  b.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  b.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(o + gw * D)[lane] = b;
+}
+
+// ------------------------------------------------------------------ fp32, CUDA cores
+
+constexpr int FM = 64, FN = 64, FTHREADS = 256;
+
+template <int DV>
+constexpr int f32_smem() {
+  return (3 * 64 * (32 * DV + 4) + FM * (FN + 4)) * 4;
+}
+
+// 64 query rows x 64 keys per step; thread (ty, tx) of 16 x 16 holds 4 rows x 4 scores
+// (keys tx + 16 k) and 4 rows x 2 DV outputs.  Masked scores are skipped by weight 0 and
+// masked V rows by staging zeros for keys that no row of the tile sees; a key that only
+// some rows see and that holds a non-finite value is left out row by row.
+template <int DV>
+__global__ void __launch_bounds__(FTHREADS)
+    attn_masked_f32_kernel(const __grid_constant__ MaskedArgs a) {
+  constexpr int DD = 32 * DV, P = DD + 4, SP = FN + 4;
+  extern __shared__ __align__(16) float fsm[];
+  float* qs = fsm;
+  float* ks = qs + FM * P;
+  float* vs = ks + FN * P;
+  float* ps = vs + FN * P;
+  __shared__ int red[2][8];
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int h = blockIdx.x % a.heads;
+  const int qblocks = (a.n_q + FM - 1) / FM;
+  const int qb = qblocks - 1 - blockIdx.x / a.heads;
+  const int row0 = qb * FM;
+  const int hk = h / (a.heads / a.kv_heads);
+  const size_t ldq = (size_t)a.heads * DD, ldk = (size_t)a.kv_heads * DD;
+  const float* q = reinterpret_cast<const float*>(a.q) + (size_t)h * DD;
+  const float* k = reinterpret_cast<const float*>(a.k) + (size_t)hk * DD;
+  const float* v = reinterpret_cast<const float*>(a.v) + (size_t)hk * DD;
+  int lo[4], hi[4];
+  int u_lo = INT_MAX, u_hi = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = hi[i] = 0;
+    const int row = row0 + ty * 4 + i;
+    if (row < a.n_q) row_range(a, row, &lo[i], &hi[i]);
+    if (hi[i] > lo[i]) {
+      u_lo = min(u_lo, lo[i]);
+      u_hi = max(u_hi, hi[i]);
+    }
+  }
+  u_lo = __reduce_min_sync(0xffffffffu, u_lo);
+  u_hi = __reduce_max_sync(0xffffffffu, u_hi);
+  if ((tid & 31) == 0) {
+    red[0][tid >> 5] = u_lo;
+    red[1][tid >> 5] = u_hi;
+  }
+  for (int x = tid; x < FM * (DD / 4); x += FTHREADS) {
+    const int rr = x / (DD / 4), c = x - rr * (DD / 4);
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row0 + rr < a.n_q) f = *reinterpret_cast<const float4*>(q + (size_t)(row0 + rr) * ldq + 4 * c);
+    *reinterpret_cast<float4*>(qs + rr * P + 4 * c) = f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    u_lo = min(u_lo, red[0][w]);
+    u_hi = max(u_hi, red[1][w]);
+  }
+  const float scale = rsqrtf((float)DD);
+  const bool cap = a.softcap > 0.f;
+  const float inv_cap = cap ? 1.f / a.softcap : 0.f;
+  const float slope = a.slopes ? __ldg(a.slopes + h) : 0.f;
+  float m[4], l[4];
+  float o[4][2 * DV];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2 * DV; ++e) o[i][e] = 0.f;
+  }
+  for (int k0 = u_lo < u_hi ? u_lo / FN * FN : 0; k0 < u_hi; k0 += FN) {
+    __syncthreads();
+    bool odd = false;                                          // a non-finite V element here
+    for (int x = tid; x < FN * (DD / 4); x += FTHREADS) {
+      const int rr = x / (DD / 4), c = x - rr * (DD / 4);
+      float4 fk = make_float4(0.f, 0.f, 0.f, 0.f), fv = fk;
+      if (k0 + rr >= u_lo && k0 + rr < u_hi) {
+        fk = __ldg(reinterpret_cast<const float4*>(k + (size_t)(k0 + rr) * ldk + 4 * c));
+        fv = __ldg(reinterpret_cast<const float4*>(v + (size_t)(k0 + rr) * ldk + 4 * c));
+        odd |= !(isfinite(fv.x) && isfinite(fv.y) && isfinite(fv.z) && isfinite(fv.w));
+      }
+      *reinterpret_cast<float4*>(ks + rr * P + 4 * c) = fk;
+      *reinterpret_cast<float4*>(vs + rr * P + 4 * c) = fv;
+    }
+    odd = __syncthreads_or(odd);
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < DD; d += 4) {
+      float4 qa[4], kb[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const float4*>(qs + (ty * 4 + i) * P + d);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) kb[c] = *reinterpret_cast<const float4*>(ks + (tx + 16 * c) * P + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[i][c] = fmaf(qa[i].x, kb[c].x, s[i][c]);
+          s[i][c] = fmaf(qa[i].y, kb[c].y, s[i][c]);
+          s[i][c] = fmaf(qa[i].z, kb[c].z, s[i][c]);
+          s[i][c] = fmaf(qa[i].w, kb[c].w, s[i][c]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int pos = a.n_kv - a.n_q + row0 + ty * 4 + i;
+      float mx = m[i];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int key = k0 + tx + 16 * c;
+        float z = s[i][c] * scale;
+        if (cap) z = a.softcap * tanhf(z * inv_cap);
+        z = fmaf(-slope, fabsf((float)(pos - key)), z) * kLog2e;
+        s[i][c] = key >= lo[i] && key < hi[i] ? z : -INFINITY;
+        mx = fmaxf(mx, s[i][c]);
+      }
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      const float mb = mx == -INFINITY ? 0.f : mx;
+      const float al = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - mb);
+      m[i] = mx;
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float p = ex2_approx(s[i][c] - mb);
+        sum += p;
+        ps[(ty * 4 + i) * SP + tx + 16 * c] = p;
+      }
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l[i] = fmaf(l[i], al, sum);
+#pragma unroll
+      for (int e = 0; e < 2 * DV; ++e) o[i][e] *= al;
+    }
+    __syncwarp();                                              // a row's 16 threads share a warp
+    if (!odd) {
+#pragma unroll 2
+      for (int kk = 0; kk < FN; kk += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(ps + (ty * 4 + i) * SP + kk);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+#pragma unroll
+          for (int e = 0; e < DV; ++e) {
+            const float2 vv = *reinterpret_cast<const float2*>(vs + (kk + x) * P + 2 * tx + 32 * e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float pw = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
+              o[i][2 * e] = fmaf(pw, vv.x, o[i][2 * e]);
+              o[i][2 * e + 1] = fmaf(pw, vv.y, o[i][2 * e + 1]);
+            }
+          }
+        }
+      }
+    } else {
+      for (int kk = 0; kk < FN; ++kk)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (k0 + kk < lo[i] || k0 + kk >= hi[i]) continue;
+          const float pw = ps[(ty * 4 + i) * SP + kk];
+#pragma unroll
+          for (int e = 0; e < DV; ++e) {
+            const float2 vv = *reinterpret_cast<const float2*>(vs + kk * P + 2 * tx + 32 * e);
+            o[i][2 * e] = fmaf(pw, vv.x, o[i][2 * e]);
+            o[i][2 * e + 1] = fmaf(pw, vv.y, o[i][2 * e + 1]);
+          }
+        }
+    }
+  }
+  float* out = reinterpret_cast<float*>(a.o) + (size_t)h * DD;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + ty * 4 + i;
+    if (row >= a.n_q) continue;
+    const bool have = l[i] > 0.f || l[i] != l[i];
+#pragma unroll
+    for (int e = 0; e < DV; ++e)
+      *reinterpret_cast<float2*>(out + (size_t)row * ldq + 2 * tx + 32 * e) =
+          have ? make_float2(o[i][2 * e] / l[i], o[i][2 * e + 1] / l[i]) : make_float2(0.f, 0.f);
+  }
+}
+
+template <int DV>
+int run_f32(const MaskedArgs& a, cudaStream_t s) {
+  constexpr int smem = f32_smem<DV>();
+  const cudaError_t e =
+      cudaFuncSetAttribute(attn_masked_f32_kernel<DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return record_cuda(e);
+  const unsigned grid = (unsigned)((a.n_q + FM - 1) / FM) * (unsigned)a.heads;
+  attn_masked_f32_kernel<DV><<<grid, FTHREADS, smem, s>>>(a);
+  return record_cuda(cudaGetLastError());
+}
+
+bool pairs_heads(int heads, int kv_heads) { return (heads / kv_heads) % 2 == 0; }
+
+int base_ctas(int n_q, int heads, int kv_heads) {
+  const bool p = pairs_heads(heads, kv_heads);
+  const int rows = p ? BQ : 2 * BQ;
+  return (n_q + rows - 1) / rows * (p ? heads / 2 : heads);
+}
+
+}  // namespace
+
+// Splits fill the SMs when the query blocks alone do not; each keeps at least two key
+// tiles of the longest possible range.
+int masked_splits(int n_q, int n_kv, int heads, int kv_heads) {
+  const int ctas = base_ctas(n_q, heads, kv_heads);
+  const int tiles = (n_kv + BKV - 1) / BKV;
+  int s = kSms / ctas;
+  if (s > tiles / 2) s = tiles / 2;
+  return s < 1 ? 1 : s > kMaxKeySplits ? kMaxKeySplits : s;
+}
+
+size_t masked_workspace(int n_q, int n_kv, int heads, int kv_heads, int head_dim, int dtype) {
+  if (dtype != SFM_DTYPE_BF16) return 0;
+  const int sp = masked_splits(n_q, n_kv, heads, kv_heads);
+  if (sp == 1) return 0;
+  const size_t b = (size_t)sp * n_q * heads * (head_dim + 1) * sizeof(float);
+  return (b + 15) / 16 * 16;
+}
+
+int launch_attention_masked_tc(const MaskedArgs& a, const CUtensorMap& mq, const CUtensorMap& mk,
+                               const CUtensorMap& mv, void* workspace, const Guard& gd, cudaStream_t s) {
+  TcArgs t{};
+  t.m = a;
+  t.paired = pairs_heads(a.heads, a.kv_heads) ? 1 : 0;
+  t.hgroups = t.paired ? a.heads / 2 : a.heads;
+  const int rows = t.paired ? BQ : 2 * BQ;
+  t.qblocks = (a.n_q + rows - 1) / rows;
+  t.n_splits = masked_splits(a.n_q, a.n_kv, a.heads, a.kv_heads);
+  const long long rows_heads = (long long)a.n_q * a.heads;
+  if (t.n_splits > 1) {
+    t.o_part = (float*)workspace;
+    t.lse_part = t.o_part + (size_t)t.n_splits * rows_heads * D;
+  }
+  t.err = gd.err;
+  t.wait_ns = gd.wait_ns;
+  t.fault = gd.fault;
+  const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
+  auto kernel = cap ? (bias ? attn_masked_tc_kernel<true, true> : attn_masked_tc_kernel<true, false>)
+                    : (bias ? attn_masked_tc_kernel<false, true> : attn_masked_tc_kernel<false, false>);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return record_cuda(e);
+  int rc;
+  {
+    ProfScope ps(SFM_PROF_ATTN, s);
+    kernel<<<(unsigned)(t.qblocks * t.hgroups * t.n_splits), THREADS, SMEM, s>>>(mq, mk, mv, t);
+    rc = record_cuda(cudaGetLastError());
+  }
+  if (rc || t.n_splits == 1) return rc;
+  ProfScope ps(SFM_PROF_ATTN_MERGE, s);
+  masked_join_kernel<<<(unsigned)((rows_heads * 32 + 255) / 256), 256, 0, s>>>(
+      t.o_part, t.lse_part, (__nv_bfloat16*)a.o, rows_heads, t.n_splits);
+  return record_cuda(cudaGetLastError());
+}
+
+int launch_attention_masked_f32(const MaskedArgs& a, cudaStream_t s) {
+  ProfScope ps(SFM_PROF_ATTN, s);
+  switch (a.head_dim / 32) {
+    case 1: return run_f32<1>(a, s);
+    case 2: return run_f32<2>(a, s);
+    case 3: return run_f32<3>(a, s);
+    default: return run_f32<4>(a, s);
+  }
+}
+
+int launch_attention_bounds(const BoundsArgs& a, cudaStream_t s) {
+  ProfScope ps(SFM_PROF_ROWOPS, s);
+  attention_bounds_kernel<<<(unsigned)((a.n_q + 255) / 256), 256, 0, s>>>(a);
+  return record_cuda(cudaGetLastError());
+}
+
+}  // namespace sfm

@@ -39,6 +39,9 @@ struct Guard {
   int fault = 0;
 };
 
+// The error word, wait bound and test-only fault of the standalone calls on the current device.
+int call_guard(Guard* gd);
+
 struct Session {
   bool open = false;
   int cache_units = 0;

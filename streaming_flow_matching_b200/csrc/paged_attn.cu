@@ -1,0 +1,805 @@
+// Attention of one new token per sequence over the paged K/V cache.
+//
+//   s_t = q . k_t / sqrt(D);  s = cap tanh(s / cap);  s -= slope_h |q_pos - pos_t|
+//   O = sum_t softmax(s)_t v_t over the sequence's slots;  weights[t] += sum of the
+//   softmax over the query heads that share the key head.
+//
+// Bound by reading K and V once: with G query heads per key head every 2-byte element
+// takes part in 2 G operations, far below the tensor cores' ratio but above the CUDA
+// cores' for G >= 4, so bf16 uses mma.sync m16n8k16 (a tcgen05 tile would be 128 rows
+// high for G rows of work, and its round trips through TMEM add latency that the copy
+// rate does not leave).  Both products are transposed so that the tile's long side is
+// the matrix's M: S^T = K Q^T (16 tokens x 8 heads), O^T = V^T P^T (16 dims x 8 heads);
+// P^T gets from the accumulator to the operand layout through movmatrix, in registers.
+// P is used as a bf16 pair hi + lo (two products, 2^-15 of p left out): its rounding to one
+// bf16 would be as large as the output's own, and the tensor cores wait for memory anyway.
+//
+// Work split: the sequences' 64-token tiles, all laid end to end, are cut into `slots`
+// equal runs (lengths are read on the device, so ragged batches stay balanced and a
+// captured graph follows the lengths); CTA (slot, head) walks its run.  The heads of
+// one slot are neighbours in the grid: they read neighbouring 256-byte pieces of the
+// same rows at about the same time.  A CTA's four warps take 16 tokens of each tile,
+// each with its own ring of cp.async stages (no barrier until a sequence ends).  A
+// sequence inside one run is finished there; otherwise its fp32 partials are joined by
+// a second kernel, in slot order, so results do not depend on timing.
+#include <math.h>
+
+#include "paged.cuh"
+#include "sm100.cuh"
+
+namespace sfm {
+
+using sm100::ex2_approx;
+using sm100::smem_u32;
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kWarpTok = 16, kTile = kWarps * kWarpTok;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.f;     // a running max is moved once a score passes it by 2^8
+constexpr float kHiPart = -0x1.fffffep-1f;   // -(1 - 2^-24)
+constexpr int kSms = 148;
+
+// What the kernels share about the split of one call.
+struct Split {
+  int slots;            // runs of tiles
+  int hgroups;          // head groups: key heads x tiles of query heads
+  int gt;               // query-head tiles per key head
+  int hpt;              // query heads per tile
+  float* part;          // [slots][hgroups][2][hpt][D]
+  float* ml;            // [slots][hgroups][2][hpt][2]: running max (log2), sum
+  float* lse;           // [n_seq][H] (log2; with weights)
+  float* scores;        // [n_seq][H][max_tokens] (log2; with weights)
+};
+
+// Number of tiles of all sequences, by one warp.
+__device__ int total_tiles(const PagedCache& c, int lane, int* err) {
+  int sum = 0;
+  for (int s = lane; s < c.n_seq; s += 32) sum += (cache_len(c, s, err) + kTile - 1) / kTile;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// The sequence that holds tile b of all (b < total) and that tile's index in it, by one warp.
+__device__ void find_tile(const PagedCache& c, int b, int lane, int* seq, int* tile) {
+  int base = 0;
+  for (int s0 = 0; s0 < c.n_seq; s0 += 32) {
+    const int s = s0 + lane;
+    const int nt = s < c.n_seq ? (cache_len(c, s, nullptr) + kTile - 1) / kTile : 0;
+    int inc = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, base + inc > b);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      *seq = s0 + l;
+      *tile = b - base - __shfl_sync(0xffffffffu, inc - nt, l);
+      return;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  *seq = c.n_seq;     // not reached for b < total
+  *tile = 0;
+}
+
+// A walk over tiles in order: sequence, tile in it, its length.
+struct Walk {
+  int seq, tile, len;
+  __device__ __forceinline__ void next(const PagedCache& c) {
+    ++tile;
+    if (tile * kTile < len) return;
+    tile = 0;
+    do {
+      ++seq;
+      len = seq < c.n_seq ? cache_len(c, seq, nullptr) : 0;
+    } while (len == 0 && seq < c.n_seq);
+  }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// One score in log2 units.  The distance is taken in whole numbers first: a slope times
+// an absolute position would lose what tells neighbours apart.
+template <bool CAP>
+__device__ __forceinline__ float finish_score(float dot, float scale, float cap, float inv_cap, float slope,
+                                              float dist) {
+  float s = dot * scale;
+  if (CAP) s = cap * tanhf(s * inv_cap);
+  return fmaf(-slope, dist, s) * kLog2e;
+}
+
+// Writes head `h` (of the tile, D values held one per thread tid < D) of a finished or
+// partial sequence.  first: the run's first tile of the sequence is not its tile 0.
+struct Segment {
+  bool starts_before, ends_after;
+  __device__ bool partial() const { return starts_before || ends_after; }
+  __device__ int index() const { return starts_before ? 0 : 1; }
+};
+
+// ------------------------------------------------------------------ bf16, D = 128
+
+constexpr int kStages = 3;
+constexpr int kStageBytes = 2 * kWarpTok * 256;                 // K and V rows of 16 tokens
+constexpr int kOPitch = 132;                                    // floats per head row of the merge buffer
+constexpr int kOffMerge = kWarps * kStages * kStageBytes;       // 96 KB of rings, then
+constexpr int kOffMl = kOffMerge + kWarps * 8 * kOPitch * 4;    // O^T of each warp, its max and sum
+constexpr int kSmemBf16 = kOffMl + kWarps * 8 * 2 * 4;          // 115,456 bytes: two CTAs per SM
+
+template <int NT, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_attn_bf16_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int hg = blockIdx.x % sp.hgroups, slot = blockIdx.x / sp.hgroups;
+  const int hk = hg / sp.gt;                                  // key head
+  const int G = a.heads / a.c.kv_heads;
+  const int g0 = (hg - hk * sp.gt) * (8 * NT);                // first query head of the group here
+  const int nh = min(8 * NT, G - g0);                         // query heads of this tile
+  const int h0 = hk * G + g0;
+  const int total = total_tiles(a.c, lane, a.err);
+  const int chunk = (total + sp.slots - 1) / sp.slots;
+  const int b0 = slot * chunk, b1 = min(total, b0 + chunk);
+  if (b0 >= b1) return;
+
+  Walk ld;                                                    // of the loads
+  find_tile(a.c, b0, lane, &ld.seq, &ld.tile);
+  ld.len = cache_len(a.c, ld.seq, nullptr);
+  Walk cw = ld;                                               // of the arithmetic
+  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (kStages * kStageBytes);
+  const __nv_bfloat16* kp = reinterpret_cast<const __nv_bfloat16*>(a.k_pages) + (size_t)hk * 128;
+  const __nv_bfloat16* vp = reinterpret_cast<const __nv_bfloat16*>(a.v_pages) + (size_t)hk * 128;
+  const size_t row_elems = (size_t)a.c.kv_heads * 128;
+
+  // pool row of this lane's token (lanes 0..15) of the next tile to load; -1: none
+  auto lookup = [&](const Walk& w) -> int {
+    const int t = w.tile * kTile + warp * kWarpTok + (lane & 15);
+    return lane < 16 && t < w.len ? cache_row(a.c, w.seq, t, a.err) : -1;
+  };
+  // a tile's 16 K rows and 16 V rows: lane = 16-byte piece (lane & 15) of rows (lane >> 4) + 2 i;
+  // pieces are stored at piece ^ (row & 7): no bank conflicts for ldmatrix, either way round
+  auto issue = [&](int stage, int row) {
+    const uint32_t dst = ring + (uint32_t)stage * kStageBytes;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int rr = 2 * i + (lane >> 4);
+      const int row_i = __shfl_sync(0xffffffffu, row, rr);
+      const size_t off = (size_t)max(row_i, 0) * row_elems + (lane & 15) * 8;
+      const uint32_t d = dst + (uint32_t)(rr * 256 + (((lane & 15) ^ (rr & 7)) << 4));
+      cp_async16(d, kp + off, row_i >= 0);
+      cp_async16(d + kWarpTok * 256, vp + off, row_i >= 0);
+    }
+  };
+
+  const int n_tiles = b1 - b0;
+  unsigned masks[kStages] = {};                               // which of the 16 tokens count
+  int next_row = lookup(ld);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    masks[i] = 0;
+    if (i < n_tiles) {
+      masks[i] = __ballot_sync(0xffffffffu, next_row >= 0) & 0xffffu;
+      issue(i, next_row);
+      if (i + 1 < n_tiles) {
+        ld.next(a.c);
+        next_row = lookup(ld);
+      }
+    }
+    cp_commit();
+  }
+
+  uint32_t qf[8][NT][2];                                      // Q^T operand of the current sequence
+  float acc[8][NT][4];                                        // O^T: dims 16 i + g (+8), heads 2 t4 (+1)
+  float m[NT][2], l[NT][2], slope[NT][2];
+  bool fresh = true;
+  const float scale = 0.08838834764831845f;                   // 1 / sqrt(128)
+  const float inv_cap = CAP ? 1.f / a.softcap : 0.f;
+  int q_pos = 0;
+  bool seg_start = false;
+
+  for (int it = 0; it < n_tiles; ++it) {
+    if (fresh) {
+      fresh = false;
+      seg_start = cw.tile != 0;                               // an earlier run has its first tiles
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)cw.seq * a.heads + h0) * 64;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const bool have = nt * 8 + g < nh;                    // heads past the group: zeros
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          qf[ks][nt][0] = have ? __ldg(q + (nt * 8 + g) * 64 + ks * 8 + t4) : 0u;
+          qf[ks][nt][1] = have ? __ldg(q + (nt * 8 + g) * 64 + ks * 8 + t4 + 4) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m[nt][e] = -INFINITY;
+          l[nt][e] = 0.f;
+          const int hh = nt * 8 + 2 * t4 + e;
+          slope[nt][e] = BIAS && hh < nh ? __ldg(a.slopes + h0 + hh) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
+      }
+      if (BIAS) q_pos = a.q_positions ? __ldg(a.q_positions + cw.seq) : cw.len - 1;
+    }
+    // keep the ring full: the tile kStages - 1 ahead goes where the last one was consumed
+    if (it + kStages - 1 < n_tiles) {
+      masks[kStages - 1] = __ballot_sync(0xffffffffu, next_row >= 0) & 0xffffu;
+      issue((it + kStages - 1) % kStages, next_row);
+      if (it + kStages < n_tiles) {
+        ld.next(a.c);
+        next_row = lookup(ld);
+      }
+    }
+    cp_commit();
+    cp_wait<kStages - 1>();
+    __syncwarp();
+
+    const uint32_t ks_base = ring + (uint32_t)(it % kStages) * kStageBytes;
+    const uint32_t vs_base = ks_base + kWarpTok * 256;
+    const int tok = cw.tile * kTile + warp * kWarpTok + g;    // this thread's tokens: tok, tok + 8
+    const unsigned mk = masks[0];
+    if (mk) {
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+      {
+        const int r = lane & 15;                              // K rows as the A operand
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          uint32_t ka[4];
+          ldsm4(ka, ks_base + (uint32_t)(r * 256 + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4)));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], ka, qf[ks][nt][0], qf[ks][nt][1]);
+        }
+      }
+      const bool in0 = (mk >> g) & 1u, in1 = (mk >> (g + 8)) & 1u;
+      float d0 = 0.f, d1 = 0.f;
+      if (BIAS) {
+        int p0 = tok, p1 = tok + 8;
+        if (a.positions) {
+          const int* ps = a.positions + ((size_t)cw.seq * a.c.kv_heads + hk) * a.cap;
+          p0 = in0 ? __ldg(ps + tok) : 0;
+          p1 = in1 ? __ldg(ps + tok + 8) : 0;
+        }
+        d0 = fabsf((float)((long long)q_pos - p0));
+        d1 = fabsf((float)((long long)q_pos - p1));
+      }
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in = e < 2 ? in0 : in1;
+          s[nt][e] = in ? finish_score<CAP>(s[nt][e], scale, a.softcap, inv_cap, slope[nt][e & 1], e < 2 ? d0 : d1)
+                        : -INFINITY;
+          grow |= s[nt][e] > m[nt][e & 1] + kGrow;            // also from m = -inf
+        }
+      if (sp.scores) {
+        // raw scores for the pass that accumulates weights: 8 consecutive tokens per head
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int hh = nt * 8 + 2 * t4 + (e & 1), tt = tok + (e >= 2 ? 8 : 0);
+            if (hh < nh && tt < cw.len)
+              sp.scores[((size_t)cw.seq * a.heads + h0 + hh) * a.c.max_tokens + tt] = s[nt][e];
+          }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(fmaxf(s[nt][e], s[nt][e + 2]), m[nt][e]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // nothing seen yet: the accumulators are zeros
+            const float al = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - mx);
+            m[nt][e] = mx;
+            l[nt][e] *= al;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[i][nt][e] *= al;
+              acc[i][nt][e + 2] *= al;
+            }
+          }
+      }
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mb = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
+          p[e] = ex2_approx(s[nt][e] - mb);
+          l[nt][e & 1] += p[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // hi by truncation and lo = p - hi (1 - 2^-24): both positive wherever p is, so that
+          // an infinite V element stays infinite (0 x inf, or inf - inf, would not)
+          const uint32_t hi = __byte_perm(__float_as_uint(p[2 * e]), __float_as_uint(p[2 * e + 1]), 0x7632);
+          const float r0 = fmaf(__uint_as_float(hi << 16), kHiPart, p[2 * e]);
+          const float r1 = fmaf(__uint_as_float(hi & 0xffff0000u), kHiPart, p[2 * e + 1]);
+          ph[nt][e] = transpose8x8(hi);
+          pl[nt][e] = transpose8x8(sm100::pack_bf16x2(r0, r1));
+        }
+      }
+      {
+        const int r = (lane & 7) + ((lane >> 4) << 3);        // V rows as the transposed A operand
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t va[4];
+          ldsm4_t(va, vs_base + (uint32_t)(r * 256 + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) << 4)));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(acc[i][nt], va, ph[nt][0], ph[nt][1]);
+            mma16816(acc[i][nt], va, pl[nt][0], pl[nt][1]);
+          }
+        }
+      }
+    }
+    __syncwarp();                                             // the stage may be refilled
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
+    const int seq = cw.seq;
+    const bool seq_done = (cw.tile + 1) * kTile >= cw.len;
+    cw.next(a.c);
+    if (!seq_done && it + 1 < n_tiles) continue;
+
+    // ---- the sequence, or the run, ends here: merge the four warps
+    fresh = true;
+    Segment sg{seg_start, !seq_done};
+    float* obuf = reinterpret_cast<float*>(smem + kOffMerge);
+    float* mlbuf = reinterpret_cast<float*>(smem + kOffMl);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = l[nt][e];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (g == 0) {
+          mlbuf[(warp * 8 + 2 * t4 + e) * 2] = m[nt][e];
+          mlbuf[(warp * 8 + 2 * t4 + e) * 2 + 1] = v;
+        }
+      }
+      float* ob = obuf + warp * 8 * kOPitch;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          ob[(2 * t4 + (e & 1)) * kOPitch + 16 * i + g + (e >> 1) * 8] = acc[i][nt][e];
+      __syncthreads();
+      const int d = threadIdx.x;
+      for (int hh = 0; hh < 8 && nt * 8 + hh < nh; ++hh) {
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mlbuf[(w * 8 + hh) * 2]);
+        const float mb = mm == -INFINITY ? 0.f : mm;
+        float sum = 0.f, o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2_approx(mlbuf[(w * 8 + hh) * 2] - mb);
+          sum = fmaf(f, mlbuf[(w * 8 + hh) * 2 + 1], sum);
+          o = fmaf(f, obuf[(w * 8 + hh) * kOPitch + d], o);
+        }
+        const int ht = nt * 8 + hh;                           // head of the tile
+        if (sg.partial()) {
+          const size_t at = (((size_t)slot * sp.hgroups + hg) * 2 + sg.index()) * sp.hpt + ht;
+          sp.part[at * 128 + d] = o;
+          if (d == 0) {
+            sp.ml[at * 2] = mm;
+            sp.ml[at * 2 + 1] = sum;
+          }
+        } else {
+          reinterpret_cast<__nv_bfloat16*>(a.o)[((size_t)seq * a.heads + h0 + ht) * 128 + d] =
+              __float2bfloat16(sum > 0.f || sum != sum ? o / sum : 0.f);
+          if (sp.lse && d == 0) sp.lse[(size_t)seq * a.heads + h0 + ht] = mb + log2f(sum);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  cp_wait<0>();
+}
+
+// ------------------------------------------------------------------ fp32, D = 32 DV
+
+// CUDA cores.  A warp takes 4 tokens at a time, 8 lanes to a token: lane j of the eight
+// holds the 16-byte pieces j + 8 i of the row, so a load instruction covers whole
+// 128-byte lines, and a score takes three shuffles for four tokens.  GT query heads per
+// CTA (a larger group reads its keys again, from L2).
+template <int DV, int GT>
+__global__ void __launch_bounds__(kThreads)
+    paged_attn_fp32_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp) {
+  constexpr int D = 32 * DV;
+  __shared__ float4 qs[GT][D / 4];
+  __shared__ float obuf[kWarps][GT][D];
+  __shared__ float mlbuf[kWarps][GT][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = lane & 7, grp = lane >> 3;
+  const int hg = blockIdx.x % sp.hgroups, slot = blockIdx.x / sp.hgroups;
+  const int hk = hg / sp.gt;
+  const int G = a.heads / a.c.kv_heads;
+  const int g0 = (hg - hk * sp.gt) * GT;
+  const int nh = min(GT, G - g0);
+  const int h0 = hk * G + g0;
+  const int total = total_tiles(a.c, lane, a.err);
+  const int chunk = (total + sp.slots - 1) / sp.slots;
+  const int b0 = slot * chunk, b1 = min(total, b0 + chunk);
+  if (b0 >= b1) return;
+  Walk cw;
+  find_tile(a.c, b0, lane, &cw.seq, &cw.tile);
+  cw.len = cache_len(a.c, cw.seq, nullptr);
+  const size_t row_vecs = (size_t)a.c.kv_heads * (D / 4);
+  const float4* kp = reinterpret_cast<const float4*>(a.k_pages) + (size_t)hk * (D / 4);
+  const float4* vp = reinterpret_cast<const float4*>(a.v_pages) + (size_t)hk * (D / 4);
+  const float scale = rsqrtf((float)D);
+  const bool cap = a.softcap > 0.f;
+  const float inv_cap = cap ? 1.f / a.softcap : 0.f;
+
+  float4 acc[GT][DV];
+  float m[GT], l[GT], slope[GT];
+  bool fresh = true, seg_start = false;
+  int q_pos = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (fresh) {
+      fresh = false;
+      seg_start = cw.tile != 0;
+      for (int x = threadIdx.x; x < GT * (D / 4); x += kThreads) {
+        const int hh = x / (D / 4), c = x - hh * (D / 4);
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (hh < nh) f = __ldg(reinterpret_cast<const float4*>(a.q) + ((size_t)cw.seq * a.heads + h0 + hh) * (D / 4) + c);
+        qs[hh][c] = f;
+      }
+#pragma unroll
+      for (int hh = 0; hh < GT; ++hh) {
+        m[hh] = -INFINITY;
+        l[hh] = 0.f;
+        slope[hh] = a.slopes && hh < nh ? __ldg(a.slopes + h0 + hh) : 0.f;
+#pragma unroll
+        for (int i = 0; i < DV; ++i) acc[hh][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      q_pos = a.q_positions ? __ldg(a.q_positions + cw.seq) : cw.len - 1;
+      __syncthreads();
+    }
+    const int base = cw.tile * kTile + warp * kWarpTok;
+    int row16 = -1;
+    if (lane < kWarpTok && base + lane < cw.len) row16 = cache_row(a.c, cw.seq, base + lane, a.err);
+#pragma unroll
+    for (int step = 0; step < kWarpTok / 4; ++step) {
+      const int tok = base + step * 4 + grp;
+      const int row = __shfl_sync(0xffffffffu, row16, step * 4 + grp);
+      float4 kf[DV], vf[DV];
+#pragma unroll
+      for (int i = 0; i < DV; ++i) {
+        kf[i] = vf[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row >= 0) {
+          kf[i] = __ldg(kp + (size_t)row * row_vecs + j + 8 * i);
+          vf[i] = __ldg(vp + (size_t)row * row_vecs + j + 8 * i);
+        }
+      }
+      float dist = 0.f;
+      if (a.slopes && row >= 0) {
+        const int p = a.positions ? __ldg(a.positions + ((size_t)cw.seq * a.c.kv_heads + hk) * a.cap + tok) : tok;
+        dist = fabsf((float)((long long)q_pos - p));
+      }
+#pragma unroll
+      for (int hh = 0; hh < GT; ++hh) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < DV; ++i) {
+          const float4 qv = qs[hh][j + 8 * i];
+          s = fmaf(qv.x, kf[i].x, s);
+          s = fmaf(qv.y, kf[i].y, s);
+          s = fmaf(qv.z, kf[i].z, s);
+          s = fmaf(qv.w, kf[i].w, s);
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        if (row < 0) s = -INFINITY;
+        else if (cap) s = finish_score<true>(s, scale, a.softcap, inv_cap, slope[hh], dist);
+        else s = finish_score<false>(s, scale, 0.f, 0.f, slope[hh], dist);
+        if (sp.scores && j == 0 && hh < nh && tok < cw.len)
+          sp.scores[((size_t)cw.seq * a.heads + h0 + hh) * a.c.max_tokens + tok] = s;
+        if (__any_sync(0xffffffffu, s > m[hh] + kGrow)) {      // each group of 8 lanes has its own max
+          const float mx = fmaxf(m[hh], s);
+          const float al = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - mx);
+          m[hh] = mx;
+          l[hh] *= al;
+#pragma unroll
+          for (int i = 0; i < DV; ++i) {
+            acc[hh][i].x *= al;
+            acc[hh][i].y *= al;
+            acc[hh][i].z *= al;
+            acc[hh][i].w *= al;
+          }
+        }
+        const float p = ex2_approx(s - (m[hh] == -INFINITY ? 0.f : m[hh]));
+        l[hh] += p;
+#pragma unroll
+        for (int i = 0; i < DV; ++i) {
+          acc[hh][i].x = fmaf(p, vf[i].x, acc[hh][i].x);
+          acc[hh][i].y = fmaf(p, vf[i].y, acc[hh][i].y);
+          acc[hh][i].z = fmaf(p, vf[i].z, acc[hh][i].z);
+          acc[hh][i].w = fmaf(p, vf[i].w, acc[hh][i].w);
+        }
+      }
+    }
+    const int seq = cw.seq;
+    const bool seq_done = (cw.tile + 1) * kTile >= cw.len;
+    cw.next(a.c);
+    if (!seq_done && b + 1 < b1) continue;
+
+    fresh = true;
+    Segment sg{seg_start, !seq_done};
+#pragma unroll
+    for (int hh = 0; hh < GT; ++hh) {
+      // the warp's four groups, then its result to shared memory
+      float mw = m[hh];
+      mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 8));
+      mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 16));
+      const float f = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - mw);
+      float lw = l[hh] * f;
+      lw += __shfl_xor_sync(0xffffffffu, lw, 8);
+      lw += __shfl_xor_sync(0xffffffffu, lw, 16);
+#pragma unroll
+      for (int i = 0; i < DV; ++i) {
+        float v[4] = {acc[hh][i].x * f, acc[hh][i].y * f, acc[hh][i].z * f, acc[hh][i].w * f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] += __shfl_xor_sync(0xffffffffu, v[e], 8);
+          v[e] += __shfl_xor_sync(0xffffffffu, v[e], 16);
+        }
+        if (grp == 0) *reinterpret_cast<float4*>(&obuf[warp][hh][(j + 8 * i) * 4]) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+      if (lane == 0) {
+        mlbuf[warp][hh][0] = mw;
+        mlbuf[warp][hh][1] = lw;
+      }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < nh * D; x += kThreads) {
+      const int hh = x / D, d = x - hh * D;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mlbuf[w][hh][0]);
+      const float mb = mm == -INFINITY ? 0.f : mm;
+      float sum = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2_approx(mlbuf[w][hh][0] - mb);
+        sum = fmaf(f, mlbuf[w][hh][1], sum);
+        o = fmaf(f, obuf[w][hh][d], o);
+      }
+      if (sg.partial()) {
+        const size_t at = (((size_t)slot * sp.hgroups + hg) * 2 + sg.index()) * sp.hpt + hh;
+        sp.part[at * D + d] = o;
+        if (d == 0) {
+          sp.ml[at * 2] = mm;
+          sp.ml[at * 2 + 1] = sum;
+        }
+      } else {
+        reinterpret_cast<float*>(a.o)[((size_t)seq * a.heads + h0 + hh) * D + d] =
+            sum > 0.f || sum != sum ? o / sum : 0.f;
+        if (sp.lse && d == 0) sp.lse[(size_t)seq * a.heads + h0 + hh] = mb + log2f(sum);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ join
+
+// One CTA per (sequence, query head): combines the sequence's partials in slot order;
+// a sequence finished by one CTA is left alone, an empty one gets zeros.
+template <typename T>
+__global__ void __launch_bounds__(128)
+    paged_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp) {
+  grid_dependency_wait();
+  const int seq = blockIdx.x / a.heads, h = blockIdx.x - seq * a.heads;
+  const int lane = threadIdx.x & 31, d = threadIdx.x, D = a.c.head_dim;
+  const int total = total_tiles(a.c, lane, nullptr);
+  int start = 0;
+  for (int s = lane; s < seq; s += 32) start += (cache_len(a.c, s, nullptr) + kTile - 1) / kTile;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) start += __shfl_xor_sync(0xffffffffu, start, o);
+  const int nt = (cache_len(a.c, seq, nullptr) + kTile - 1) / kTile;
+  T* out = reinterpret_cast<T*>(a.o) + ((size_t)seq * a.heads + h) * D;
+  if (nt == 0) {
+    if (d < D) out[d] = (T)0.f;
+    return;
+  }
+  const int chunk = (total + sp.slots - 1) / sp.slots;
+  const int s0 = start / chunk, s1 = (start + nt - 1) / chunk;
+  if (s0 == s1) return;
+  const int G = a.heads / a.c.kv_heads;
+  const int hk = h / G, gi = h - hk * G;
+  const int hg = hk * sp.gt + gi / sp.hpt, ht = gi % sp.hpt;
+  // the run that holds tile 0 of the sequence wrote index 1, the later ones index 0
+  auto at = [&](int s) {
+    return (((size_t)s * sp.hgroups + hg) * 2 + (s == s0 ? 1 : 0)) * sp.hpt + ht;
+  };
+  float mm = -INFINITY;
+  for (int s = s0 + lane; s <= s1; s += 32) mm = fmaxf(mm, sp.ml[at(s) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+  const float mb = mm == -INFINITY ? 0.f : mm;
+  float sum = 0.f, acc = 0.f;
+#pragma unroll 4
+  for (int s = s0; s <= s1; ++s) {
+    const float f = ex2_approx(sp.ml[at(s) * 2] - mb);
+    sum = fmaf(f, sp.ml[at(s) * 2 + 1], sum);
+    if (d < D) acc = fmaf(f, sp.part[at(s) * D + d], acc);
+  }
+  if (d < D) out[d] = (T)(sum > 0.f || sum != sum ? acc / sum : 0.f);
+  if (sp.lse && d == 0) sp.lse[(size_t)seq * a.heads + h] = mb + log2f(sum);
+}
+
+// weights[seq][hk][t] += sum over the key head's query heads of 2^(score - lse).
+constexpr int kAccThreads = 256, kAccTok = 1024;
+__global__ void __launch_bounds__(kAccThreads)
+    paged_weights_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp, int blocks_per_item) {
+  grid_dependency_wait();
+  const int item = blockIdx.x / blocks_per_item, blk = blockIdx.x - item * blocks_per_item;
+  const int seq = item / a.c.kv_heads, hk = item - seq * a.c.kv_heads;
+  const int G = a.heads / a.c.kv_heads;
+  const int n = cache_len(a.c, seq, nullptr);
+  const int t1 = min(n, (blk + 1) * kAccTok);
+  const float* sc = sp.scores + ((size_t)seq * a.heads + hk * G) * a.c.max_tokens;
+  const float* lse = sp.lse + (size_t)seq * a.heads + hk * G;
+  float* w = a.weights + (size_t)item * a.cap;
+  for (int t = blk * kAccTok + threadIdx.x; t < t1; t += kAccThreads) {
+    float sum = 0.f;
+    for (int gi = 0; gi < G; ++gi) {
+      const float ls = __ldg(lse + gi);
+      // no visible token (every page bad): nothing to add
+      if (ls != -INFINITY) sum += ex2_approx(sc[(size_t)gi * a.c.max_tokens + t] - ls);
+    }
+    w[t] += sum;
+  }
+}
+
+struct Plan {
+  Split sp;
+  size_t bytes;
+};
+
+// Query heads of a CTA: bf16 in tiles of 8 (one mma column block) or 16; fp32 up to 4.
+int heads_per_tile(int G, int dtype) {
+  if (dtype == SFM_DTYPE_BF16) return G <= 8 ? 8 : 16;
+  return G >= 4 ? 4 : G >= 2 ? 2 : 1;
+}
+
+Plan make_plan(int n_seq, int max_tokens, int heads, int kv_heads, int head_dim, int dtype, bool weights,
+               void* ws) {
+  Plan p{};
+  const int G = heads / kv_heads;
+  Split& sp = p.sp;
+  sp.hpt = heads_per_tile(G, dtype);
+  sp.gt = (G + sp.hpt - 1) / sp.hpt;
+  sp.hgroups = kv_heads * sp.gt;
+  // one wave: two CTAs per SM (bf16, by shared memory), four (fp32, by registers)
+  const int ctas = kSms * (dtype == SFM_DTYPE_BF16 ? 2 : 4);
+  sp.slots = ctas / sp.hgroups < 1 ? 1 : ctas / sp.hgroups;
+  char* at = (char*)ws;
+  auto take = [&](size_t floats) {
+    float* r = (float*)at;
+    const size_t b = (floats * sizeof(float) + 15) / 16 * 16;
+    at += b;
+    p.bytes += b;
+    return r;
+  };
+  const size_t parts = (size_t)sp.slots * sp.hgroups * 2 * sp.hpt;
+  sp.part = take(parts * head_dim);
+  sp.ml = take(parts * 2);
+  if (weights) {
+    sp.lse = take((size_t)n_seq * heads);
+    sp.scores = take((size_t)n_seq * heads * max_tokens);
+  }
+  return p;
+}
+
+template <int NT>
+cudaError_t launch_bf16(const DecodeArgs& a, const Split& sp, unsigned grid, cudaStream_t s) {
+  const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
+  auto kernel = cap ? (bias ? paged_attn_bf16_kernel<NT, true, true> : paged_attn_bf16_kernel<NT, true, false>)
+                    : (bias ? paged_attn_bf16_kernel<NT, false, true> : paged_attn_bf16_kernel<NT, false, false>);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBf16);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, kSmemBf16, s>>>(a, sp);
+  return cudaGetLastError();
+}
+
+template <int DV>
+void launch_fp32(const DecodeArgs& a, const Split& sp, unsigned grid, cudaStream_t s) {
+  if (sp.hpt == 4) paged_attn_fp32_kernel<DV, 4><<<grid, kThreads, 0, s>>>(a, sp);
+  else if (sp.hpt == 2) paged_attn_fp32_kernel<DV, 2><<<grid, kThreads, 0, s>>>(a, sp);
+  else paged_attn_fp32_kernel<DV, 1><<<grid, kThreads, 0, s>>>(a, sp);
+}
+
+}  // namespace
+
+size_t paged_attention_workspace(int n_seq, int max_tokens, int heads, int kv_heads, int head_dim, int dtype,
+                                 bool weights) {
+  return make_plan(n_seq, max_tokens, heads, kv_heads, head_dim, dtype, weights, nullptr).bytes;
+}
+
+int launch_paged_attention(const DecodeArgs& a, int dtype, void* workspace, cudaStream_t s) {
+  const Split sp = make_plan(a.c.n_seq, a.c.max_tokens, a.heads, a.c.kv_heads, a.c.head_dim, dtype,
+                             a.weights != nullptr, workspace).sp;
+  const unsigned grid = (unsigned)(sp.slots * sp.hgroups);
+  int rc;
+  {
+    ProfScope ps(SFM_PROF_ATTN, s);
+    cudaError_t e = cudaSuccess;
+    if (dtype == SFM_DTYPE_BF16) {
+      e = sp.hpt == 8 ? launch_bf16<1>(a, sp, grid, s) : launch_bf16<2>(a, sp, grid, s);
+    } else {
+      switch (a.c.head_dim / 32) {
+        case 1: launch_fp32<1>(a, sp, grid, s); break;
+        case 2: launch_fp32<2>(a, sp, grid, s); break;
+        case 3: launch_fp32<3>(a, sp, grid, s); break;
+        default: launch_fp32<4>(a, sp, grid, s); break;
+      }
+      e = cudaGetLastError();
+    }
+    if ((rc = record_cuda(e))) return rc;
+  }
+  ProfScope ps(SFM_PROF_ATTN_MERGE, s);
+  const unsigned joins = (unsigned)(a.c.n_seq * a.heads);
+  if (dtype == SFM_DTYPE_BF16)
+    rc = record_cuda(launch_dependent(paged_join_kernel<__nv_bfloat16>, joins, 128, 0, s, a, sp));
+  else
+    rc = record_cuda(launch_dependent(paged_join_kernel<float>, joins, 128, 0, s, a, sp));
+  if (rc || !a.weights) return rc;
+  const int per_item = (a.c.max_tokens + kAccTok - 1) / kAccTok;
+  return record_cuda(launch_dependent(paged_weights_kernel, (unsigned)(a.c.n_seq * a.c.kv_heads * per_item),
+                                      kAccThreads, 0, s, a, sp, per_item));
+}
+
+}  // namespace sfm

@@ -372,5 +372,7 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t cta_mas
 // dims 1.. (rank - 1 entries).  Returns SFM_OK or SFM_ECUDA / SFM_EINVAL.
 int make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                    const uint64_t* strides_bytes, const uint32_t* box);
+// rows of [rows][H][128] bf16 (queries, or keys / values), box box_rows x 64 dims of one head
+int make_rows_map(CUtensorMap* map, const void* p, long long rows, int heads, int box_rows);
 
 }  // namespace sfm

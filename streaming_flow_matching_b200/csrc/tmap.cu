@@ -51,4 +51,11 @@ int make_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t*
   return r == CUDA_SUCCESS ? SFM_OK : SFM_EINVAL;
 }
 
+int make_rows_map(CUtensorMap* m, const void* p, long long rows, int heads, int box_rows) {
+  const uint64_t dims[3] = {128, (uint64_t)heads, (uint64_t)rows};
+  const uint64_t strides[2] = {256, (uint64_t)heads * 256};
+  const uint32_t box[3] = {64, 1, (uint32_t)box_rows};
+  return make_tmap_bf16(m, p, 3, dims, strides, box);
+}
+
 }  // namespace sfm
