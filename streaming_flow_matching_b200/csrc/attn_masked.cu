@@ -9,14 +9,14 @@
 // beside them.  One CTA = two 128-row query tiles over the same key tiles: two heads of
 // one group at the same rows where the group is even (both tiles then have the same
 // ranges and no key tile is loaded for the sake of one of them), else 256 rows of one
-// head.  352 threads:
+// head.  384 threads:
 //   warp 0      TMA producer: the Q tiles once, K tiles (128 keys) in a 3-stage ring, V
 //               tiles in a 2-stage ring (128-byte swizzle)
 //   warp 1      TMEM allocator; one lane issues S_t = Q_t K_j^T and O_t += P_t V_j (P from
 //               TMEM), alternating the tiles
-//   warps 2-9   softmax, thread = query row: one pass over S computes P against the
+//   warps 4-11  softmax, thread = query row: one pass over S computes P against the
 //               running max, which moves only when a score passes it by 2^8
-//   warp 10     makes V safe: a masked key has weight 0, and 0 x inf or 0 x NaN would
+//   warp 2      makes V safe: a masked key has weight 0, and 0 x inf or 0 x NaN would
 //               still reach rows that may not see it.  In key tiles that some row does not
 //               see whole it scans V and replaces non-finite elements by 0; if it found
 //               any, the rows that do see them get them added back at the end (a row's sum
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(256) attention_bounds_kernel(const __grid_cons
 // ------------------------------------------------------------------ bf16, tcgen05
 
 constexpr int BQ = 128, QT = 2, BKV = 128, D = 128;
-constexpr int THREADS = 352;
+constexpr int THREADS = 384;
 constexpr int KST = 3, VST = 2;
 constexpr int HALF = 128 * 64 * 2;
 constexpr int TILE = 2 * HALF;
@@ -119,7 +119,7 @@ __device__ __forceinline__ void row_range(const MaskedArgs& m, int i, int* lo, i
   *hi = b;
 }
 
-// keys [lo, hi) of a 32-column chunk as a bit mask (lo, hi relative to its first column)
+// columns [lo, hi) of up to 32 as a bit mask
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
   lo = max(lo, 0);
   hi = min(hi, 32);
@@ -137,11 +137,45 @@ __device__ __forceinline__ float tanh_ex2(float x) {
   return 1.f - __fdividef(2.f, e + 1.f);
 }
 
-// what turns a row's raw products into log2 scores
+// pairs of fp32 in one instruction
+struct F2 {
+  unsigned long long v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ void get(float* lo, float* hi) const {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+  }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+
+// tanh(y) = y P(y^2) on |y| <= 1, P of degree 4 fitted for the least maximum of |tanh(y) -
+// y P(y^2)| (2.8e-6; times a cap of 50 that is 2e-4 of a score in log2 units, where P's
+// rounding to bf16 is worth 6e-3)
+__device__ constexpr float kTanhC[5] = {0.999968468f, -0.332658210f, 0.129220573f, -0.043299715f, 0.008365811f};
+
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
+
+// what turns a row's raw products x into log2 scores
 struct ScoreMap {
   float sc;         // scale log2(e), or scale / cap
   float cap2;       // cap log2(e)
   float slope2;     // slope log2(e)
+  float x_lim;      // |x| up to which the polynomial serves: cap / scale
 };
 
 template <bool CAP, bool BIAS>
@@ -221,12 +255,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   // the rows' key ranges: this thread's row (softmax warps), and over the CTA's rows the
   // union and the intersection
-  const int st = (warp - 2) >> 2;                              // tile of a softmax warp
+  const int st = (warp - 4) >> 2;                              // tile of a softmax warp
   const int quarter = warp & 3;
   const int r = quarter * 32 + lane;
   int my_lo = 0, my_hi = m_.n_kv;
   bool live = false;                                           // the row exists
-  if (warp >= 2 && warp < 10) {
+  if (warp >= 4) {
     const int i = row0 + st * dr + r;
     int u_lo = INT_MAX, u_hi = 0, n_lo = 0, n_hi = INT_MAX;
     if (i < m_.n_q) {                                          // rows past the end see all, write nothing
@@ -244,10 +278,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     n_lo = __reduce_max_sync(0xffffffffu, n_lo);
     n_hi = __reduce_min_sync(0xffffffffu, n_hi);
     if (lane == 0) {
-      red[0 * 8 + warp - 2] = u_lo;
-      red[1 * 8 + warp - 2] = u_hi;
-      red[2 * 8 + warp - 2] = n_lo;
-      red[3 * 8 + warp - 2] = n_hi;
+      red[0 * 8 + warp - 4] = u_lo;
+      red[1 * 8 + warp - 4] = u_hi;
+      red[2 * 8 + warp - 4] = n_lo;
+      red[3 * 8 + warp - 4] = n_hi;
     }
   }
   tc_fence_before();
@@ -267,8 +301,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tps = (u1 - u0 + args.n_splits - 1) / args.n_splits;
   const int t0 = min(u1, u0 + split * tps);
   const int T = min(u1, t0 + tps) - t0;
-  // a key tile inside every row's range
-  auto whole = [&](int j) { return (t0 + j) * BKV >= full_lo && (t0 + j + 1) * BKV <= full_hi; };
+  // The order of the key tiles.  With a bias the nearest keys go first -- from the last
+  // row's own tile back, then on from there -- as their scores are the largest: the running
+  // max then hardly moves, where in ascending order it would in every tile of a steep head.
+  int near = 0;
+  if (BIAS && T > 0) {
+    const int pos = m_.n_kv - m_.n_q + min(row0 + (args.paired ? BQ : 2 * BQ), m_.n_q) - 1;
+    near = min(max(pos / BKV - t0, 0), T - 1);
+  }
+  auto tile_at = [&](int i) { return !BIAS ? t0 + i : t0 + (i <= near ? near - i : i); };
+  // a key tile (the j-th in order) inside every row's range
+  auto whole = [&](int j) {
+    const int k = tile_at(j) * BKV;
+    return k >= full_lo && k + BKV <= full_hi;
+  };
 
   if (warp == 0) {
     if (lane == 0 && T > 0 && !(args.fault & SFM_FAULT_ATTN_NO_LOADS)) {
@@ -287,8 +333,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t par = (uint32_t)((i / KST) & 1);
         if (!mbar_wait(&k_empty[s], par ^ 1u, abort, args.err, 0x401, args.wait_ns)) return false;
         mbar_arrive_expect_tx(&k_full[s], TILE);
-        tma_load_3d(base + OFF_K + s * TILE, &map_k, &k_full[s], 0, hk, (t0 + i) * BKV);
-        tma_load_3d(base + OFF_K + s * TILE + HALF, &map_k, &k_full[s], 64, hk, (t0 + i) * BKV);
+        tma_load_3d(base + OFF_K + s * TILE, &map_k, &k_full[s], 0, hk, tile_at(i) * BKV);
+        tma_load_3d(base + OFF_K + s * TILE + HALF, &map_k, &k_full[s], 64, hk, tile_at(i) * BKV);
         kp[s] = (int)par;
         return true;
       };
@@ -297,8 +343,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t par = (uint32_t)((i / VST) & 1);
         if (!mbar_wait(&v_empty[s], par ^ 1u, abort, args.err, 0x402, args.wait_ns)) return false;
         mbar_arrive_expect_tx(&v_full[s], TILE);
-        tma_load_3d(base + OFF_V + s * TILE, &map_v, &v_full[s], 0, hk, (t0 + i) * BKV);
-        tma_load_3d(base + OFF_V + s * TILE + HALF, &map_v, &v_full[s], 64, hk, (t0 + i) * BKV);
+        tma_load_3d(base + OFF_V + s * TILE, &map_v, &v_full[s], 0, hk, tile_at(i) * BKV);
+        tma_load_3d(base + OFF_V + s * TILE + HALF, &map_v, &v_full[s], 64, hk, tile_at(i) * BKV);
         vp[s] = (int)par;
         return true;
       };
@@ -389,7 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_drain(drain, 0, args.wait_ns);
       }
     }
-  } else if (warp == 10) {
+  } else if (warp == 2) {
     // ---------------- V made safe ----------------
     for (int j = 0; j < T; ++j) {
       const int vs = j % VST;
@@ -420,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_ok[vs]);
     }
-  } else {
+  } else if (warp >= 4) {
     // ---------------- softmax + output (thread = query row of tile st) ----------------
     const int t = st;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -436,11 +482,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     sm.sc = CAP ? scale / m_.softcap : scale * kLog2e;
     sm.cap2 = m_.softcap * kLog2e;
     sm.slope2 = BIAS ? __ldg(m_.slopes + h) * kLog2e : 0.f;
+    sm.x_lim = CAP ? m_.softcap / scale : 0.f;
+    F2 poly[5];                                                // kTanhC in terms of x, times cap log2(e)
+    if (CAP) {
+      const float y2 = sm.sc * sm.sc;
+      float f = sm.cap2 * sm.sc;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        poly[i] = F2(kTanhC[i] * f, kTanhC[i] * f);
+        f *= y2;
+      }
+    }
+    const F2 sc2(sm.sc, sm.sc);
     const int my_pos = m_.n_kv - m_.n_q + row_t + r;
+    const int w_pos0 = my_pos - lane, w_pos1 = w_pos0 + 31;    // positions of the warp's rows
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < T && ok; ++j) {
-      const int key0 = (t0 + j) * BKV;
+      const int key0 = tile_at(j) * BKV;
       const bool masked = !(key0 >= w_lo && key0 + BKV <= w_hi);
       const bool nothing = key0 >= any_hi || key0 + BKV <= any_lo;
       const int lo = my_lo - key0, hi = my_hi - key0;
@@ -457,9 +516,22 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[c][i] = 0u;
       } else {
-        // P = 2^(z - m); masked columns give 0.  Returns the row's sum.
-        auto attempt = [&](float neg_m) -> float {
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        // P = 2^(z - m) of the 128 columns; masked ones give 0.  Returns the row's sum.
+        // Where the warp's rows lie on one side of the keys the bias is linear in the column
+        // (|slope fq| is kept below 2^14, so that the sum rounds at 2^-10 at most).
+        const float side = key0 + BKV - 1 <= w_pos0 ? 1.f : key0 >= w_pos1 ? -1.f : 0.f;
+        const bool linear =
+            !BIAS || (side != 0.f && __all_sync(0xffffffffu, fabsf(sm.slope2 * fq) < 16384.f));
+        // FAST: the bias linear, the cap by polynomial (x_top then holds the row's largest |x|:
+        // past x_lim the result does not stand); else the general form.
+        float x_top = 0.f;
+        auto attempt = [&](float neg_m, auto is_masked, auto is_fast) -> float {
+          constexpr bool MASKED = decltype(is_masked)::value, FAST = decltype(is_fast)::value;
+          F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+          float tilt = sm.slope2 * side, fql = fq;             // z gains tilt (col - fq)
+          asm volatile("" : "+f"(tilt), "+f"(fql));            // 128 columns' terms are not worth keeping
+          const float t0 = BIAS && FAST ? fmaf(-tilt, fql, neg_m) : neg_m;
+          if (CAP && FAST) x_top = 0.f;
           uint32_t u[2][32];
           tmem_ld32(tmem + lane_base + col_s, u[0]);
           tmem_wait_ld(u[0]);
@@ -467,71 +539,102 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int c = 0; c < 4; ++c) {
             if (c + 1 < 4) tmem_ld32(tmem + lane_base + col_s + (c + 1) * 32, u[(c + 1) & 1]);
             const float* sv = reinterpret_cast<const float*>(u[c & 1]);
-            const uint32_t bits = masked ? range_bits(lo - c * 32, hi - c * 32) : 0xffffffffu;
+            const uint32_t bits = MASKED ? range_bits(lo - c * 32, hi - c * 32) : 0u;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              float p[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int col = 2 * i + e;
-                float z = score2<CAP, BIAS>(sm, sv[col], fq, (float)(c * 32 + col)) + neg_m;
-                if (masked && !((bits >> col) & 1u)) z = -INFINITY;
-                p[e] = ex2_approx(z);
-                l4[col & 3] += p[e];
+              F2 t(t0, t0);
+              if (BIAS) {
+                const float c0 = (float)(c * 32 + 2 * i), c1 = c0 + 1.f;
+                t = FAST ? F2(fmaf(tilt, c0, t0), fmaf(tilt, c1, t0))
+                         : F2(fmaf(-sm.slope2, fabsf(fql - c0), t0), fmaf(-sm.slope2, fabsf(fql - c1), t0));
               }
-              pk[c][i] = pack_bf16x2(p[0], p[1]);
+              const float x0 = sv[2 * i], x1 = sv[2 * i + 1];
+              const F2 x(x0, x1);
+              F2 z;
+              if (!CAP) {
+                z = fma2(x, sc2, t);
+              } else if (FAST) {
+                x_top = fmax3(x_top, fabsf(x0), fabsf(x1));
+                const F2 y2 = mul2(x, x);
+                F2 w = poly[4];
+#pragma unroll
+                for (int k = 3; k >= 0; --k) w = fma2(w, y2, poly[k]);
+                z = fma2(x, w, t);
+              } else {
+                z = fma2(F2(sm.cap2, sm.cap2), F2(tanh_ex2(x0 * sm.sc), tanh_ex2(x1 * sm.sc)), t);
+              }
+              float p0, p1;
+              z.get(&p0, &p1);
+              if (MASKED) {
+                if (!((bits >> (2 * i)) & 1u)) p0 = -INFINITY;
+                if (!((bits >> (2 * i + 1)) & 1u)) p1 = -INFINITY;
+              }
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              sum[i & 1] = add2(sum[i & 1], F2(p0, p1));
+              pk[c][i] = pack_bf16x2(p0, p1);
             }
             if (c + 1 < 4) tmem_wait_ld(u[(c + 1) & 1]);
           }
-          return (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          float a0, a1;
+          add2(sum[0], sum[1]).get(&a0, &a1);
+          return a0 + a1;
         };
         auto row_max = [&]() -> float {                        // of the visible scores
           float mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[32];
-            tmem_ld32(tmem + lane_base + col_s + c * 32, w);
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[16];
+            tmem_ld16(tmem + lane_base + col_s + c * 16, w);
             tmem_wait_ld(w);
             const float* sv = reinterpret_cast<const float*>(w);
-            const uint32_t bits = masked ? range_bits(lo - c * 32, hi - c * 32) : 0xffffffffu;
+            const uint32_t bits = range_bits(lo - c * 16, hi - c * 16);
+            const float fc = fq - (float)(c * 16);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float z = score2<CAP, BIAS>(sm, sv[i], fq, (float)(c * 32 + i));
+            for (int i = 0; i < 16; ++i) {
+              const float z = score2<CAP, BIAS>(sm, sv[i], fc, (float)i);
               if ((bits >> i) & 1u) mx = fmaxf(mx, z);
             }
           }
           return mx;
         };
         float lt = 0.f;
-        bool again = m == -INFINITY;                           // no max yet: take it first
-        if (!__all_sync(0xffffffffu, again)) {
-          lt = attempt(m == -INFINITY ? 0.f : -m);
-          // a score can only have passed the max by 2^8 if the row's sum did
-          again = again || !(lt <= 256.f);
-        }
-        if (__any_sync(0xffffffffu, again)) {
-          const float mx = row_max();
-          const bool grown = mx > m + kRescaleLog2;            // also from m = -inf
-          if (__any_sync(0xffffffffu, grown)) {
-            const float m_new = fmaxf(m, mx);
-            const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);   // O, l are 0 then
-            l *= alpha;
-            m = m_new;
-            if (j > 0) {
-              // O_t's previous P V has completed (S_t(j) was issued after it): rescale it
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tmem + lane_base + col_o + c * 32, o);
-                tmem_wait_ld(o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st32(tmem + lane_base + col_o + c * 32, o);
-              }
+        // a warp none of whose rows has a max yet takes it first
+        bool done = !__all_sync(0xffffffffu, m == -INFINITY);
+        for (int round = done ? 0 : 1; round < 3; ++round) {
+          if (round != 1) {
+            const float neg_m = m == -INFINITY ? 0.f : -m;
+            bool general = !linear;
+            if (linear) {
+              lt = masked ? attempt(neg_m, Yes{}, Yes{}) : attempt(neg_m, No{}, Yes{});
+              if (CAP) general = __any_sync(0xffffffffu, !(x_top <= sm.x_lim));
             }
-            lt = attempt(m == -INFINITY ? 0.f : -m);
-          } else if (__all_sync(0xffffffffu, m == -INFINITY)) {
-            lt = attempt(0.f);                                 // every score seen is -inf or masked
+            if ((CAP || BIAS) && general) lt = attempt(neg_m, Yes{}, No{});
+            // a score can only have passed the max by 2^8 if the row's sum did
+            if (round == 2 || !__any_sync(0xffffffffu, m == -INFINITY || !(lt <= 256.f))) break;
+          } else {
+            const float mx = row_max();
+            const bool grown = mx > m + kRescaleLog2;          // also from m = -inf
+            if (__any_sync(0xffffffffu, grown)) {
+              const float m_new = fmaxf(m, mx);
+              const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);   // O, l are 0 then
+              l *= alpha;
+              m = m_new;
+              if (j > 0) {
+                // O_t's previous P V has completed (S_t(j) was issued after it): rescale it
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t o[32];
+                  tmem_ld32(tmem + lane_base + col_o + c * 32, o);
+                  tmem_wait_ld(o);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                  tmem_st32(tmem + lane_base + col_o + c * 32, o);
+                }
+              }
+            } else if (done) {
+              break;                                           // the first attempt stands
+            }
           }
         }
         l += lt;
@@ -555,7 +658,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (ok) {
       // stage the warp's 32 normalised rows in shared memory (the Q and K stages, which
       // nothing reads any more), then write whole rows; float4 slot q of row i is at q ^ i
-      float4* stage = reinterpret_cast<float4*>(smem + OFF_Q) + (warp - 2) * (32 * 32);
+      float4* stage = reinterpret_cast<float4*>(smem + OFF_Q) + (warp - 4) * (32 * 32);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t u[32];
@@ -586,8 +689,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int lo = __shfl_sync(0xffffffffu, my_lo, rr), hi = __shfl_sync(0xffffffffu, my_hi, rr);
           for (int j = 0; j < T; ++j) {
             if (whole(j)) continue;
-            const int k1 = min(hi, (t0 + j + 1) * BKV);
-            for (int k = max(lo, (t0 + j) * BKV); k < k1; ++k) {
+            const int k0 = tile_at(j) * BKV, k1 = min(hi, k0 + BKV);
+            for (int k = max(lo, k0); k < k1; ++k) {
               const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(m_.v) +
                                                               ((size_t)k * m_.kv_heads + hk) * D + 4 * lane);
               if (nonfinite16(x.x) || nonfinite16(x.y)) {

@@ -7,70 +7,83 @@ returns 0x301 / 0x302 after a bad page / a length that the cache does not hold.
 """
 from __future__ import annotations
 
+from functools import lru_cache
+
 import torch
 
 from . import _lib as L
 from .performer import _DT, _need
 
-
-def _here(t, name):
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _raw_stream():
-    return torch.cuda.current_stream().cuda_stream
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+# pure functions of the shape, asked for by every call
+_attention_bytes = lru_cache(4096)(L.lib.sfm_paged_attention_workspace_bytes)
+_evict_bytes = lru_cache(4096)(L.lib.sfm_paged_evict_workspace_bytes)
+_masked_bytes = lru_cache(4096)(L.lib.sfm_attention_masked_workspace_bytes)
 
 
-def _opt(t, dtype, name, shape):
-    """Data pointer of an optional tensor, checked; 0 where there is none."""
-    if t is None:
-        return 0
+def _raw_stream(dev):
+    """The current stream's handle, without building a Stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _ptr(t, dtype, name, shape, dev):
+    """Data pointer of a contiguous tensor of this type and shape on device `dev`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape
+            and t.is_contiguous() and t.get_device() == dev):
+        return t.data_ptr()
     _need(t, dtype, name, shape)
-    _here(t, name)
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _dtype(t, name):
+def _opt(t, dtype, name, shape, dev):
+    return 0 if t is None else _ptr(t, dtype, name, shape, dev)
+
+
+def _dims(t, n, name, what):
     if not isinstance(t, torch.Tensor) or t.dtype not in _DT:
         raise ValueError(f"{name} must be a bf16 or fp32 tensor")
-    return _DT[t.dtype]
+    if t.dim() != n:
+        raise ValueError(f"{name} must be {what}")
+    return t.shape
 
 
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, dev):
+    """(tensor to keep until the launch, pointer, bytes) of the caller's workspace or a new one."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _need(workspace, workspace.dtype, "workspace")
-    _here(workspace, "workspace")
-    return workspace
+        if not need:
+            return None, 0, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), need
+    _ptr(workspace, workspace.dtype, "workspace", workspace.shape, dev)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _pools(k_pages, v_pages, table, lengths):
-    """(dtype, n_seq, n_pages, page_size, max_pages, kv_heads, head_dim) of a cache."""
-    dt = _dtype(k_pages, "k_pages")
-    if k_pages.dim() != 4 or not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("k_pages must be [n_pages][page_size][kv_heads][head_dim] and table [n_seq][max_pages]")
-    _need(k_pages, k_pages.dtype, "k_pages")
-    _need(v_pages, k_pages.dtype, "v_pages", k_pages.shape)
-    _need(table, torch.int32, "table")
-    _need(lengths, torch.int32, "lengths", (table.shape[0],))
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages"), (table, "table"), (lengths, "lengths")):
-        _here(t, name)
-    return (dt, table.shape[0], k_pages.shape[0], k_pages.shape[1], table.shape[1], k_pages.shape[2],
-            k_pages.shape[3])
+def _result(out, like, dev):
+    if out is None:
+        return torch.empty_like(like)
+    _ptr(out, like.dtype, "out", like.shape, dev)
+    return out
 
 
-def _capacity(positions, weights, n_seq, kv_heads):
-    """Slots that the state arrays hold (their last dimension), 0 without any."""
+def _width(table):
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be an int32 tensor [n_seq][max_pages]")
+    return table.shape
+
+
+def _capacity(positions, weights, n_seq, kv_heads, dev):
+    """(slots that the state arrays hold, or 0 without any; positions' pointer; weights')."""
     cap = 0
     for t, name in ((positions, "positions"), (weights, "weights")):
         if t is not None:
-            if t.dim() != 3 or (cap and t.shape[2] != cap):
+            if not isinstance(t, torch.Tensor) or t.dim() != 3 or (cap and t.shape[2] != cap):
                 raise ValueError(f"{name} must be [n_seq][kv_heads][cap], cap the same for both state arrays")
             cap = t.shape[2]
-            if tuple(t.shape) != (n_seq, kv_heads, cap):
-                raise ValueError(f"{name} must have shape {(n_seq, kv_heads, cap)}, got {tuple(t.shape)}")
-    return cap
+    shape = (n_seq, kv_heads, cap)
+    return cap, _opt(positions, _I32, "positions", shape, dev), _opt(weights, _F32, "weights", shape, dev)
+
+
+_POOL = "[n_pages][page_size][kv_heads][head_dim]"
 
 
 def paged_append(k, v, k_pages, v_pages, table, lengths, *, row_starts=None, positions=None,
@@ -81,19 +94,19 @@ def paged_append(k, v, k_pages, v_pages, table, lengths, *, row_starts=None, pos
     become pos0[s] + i (None: lengths[s] + i) and their weights 0 where those arrays are
     given.  `lengths` is the count before the call and is not changed.
     """
-    dt, n_seq, n_pages, page, width, hk, d = _pools(k_pages, v_pages, table, lengths)
-    n_rows = k.shape[0]
-    _need(k, k_pages.dtype, "k", (n_rows, hk, d))
-    _need(v, k_pages.dtype, "v", k.shape)
-    _here(k, "k")
-    _here(v, "v")
-    cap = _capacity(positions, weights, n_seq, hk)
+    dev = torch.cuda.current_device()
+    n_pages, page, hk, d = pool = _dims(k_pages, 4, "k_pages", _POOL)
+    dt = k_pages.dtype
+    n_seq, width = _width(table)
+    n_rows = _dims(k, 3, "k", "[n_rows][kv_heads][head_dim]")[0]
+    rows = (n_rows, hk, d)
+    cap, pos, wts = _capacity(positions, weights, n_seq, hk, dev)
     L.check(L.lib.sfm_paged_append(
-        k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(),
-        lengths.data_ptr(), _opt(row_starts, torch.int32, "row_starts", (n_seq + 1,)), n_rows, n_seq,
-        n_pages, page, width, hk, d, dt, _opt(positions, torch.int32, "positions", None),
-        _opt(pos0, torch.int32, "pos0", (n_seq,)), _opt(weights, torch.float32, "weights", None), cap,
-        _raw_stream()), "sfm_paged_append")
+        _ptr(k, dt, "k", rows, dev), _ptr(v, dt, "v", rows, dev), _ptr(k_pages, dt, "k_pages", pool, dev),
+        _ptr(v_pages, dt, "v_pages", pool, dev), _ptr(table, _I32, "table", (n_seq, width), dev),
+        _ptr(lengths, _I32, "lengths", (n_seq,), dev), _opt(row_starts, _I32, "row_starts", (n_seq + 1,), dev),
+        n_rows, n_seq, n_pages, page, width, hk, d, _DT[dt], pos, _opt(pos0, _I32, "pos0", (n_seq,), dev), wts,
+        cap, _raw_stream(dev)), "sfm_paged_append")
 
 
 def paged_attention(q, k_pages, v_pages, table, lengths, *, softcap=0.0, slopes=None, positions=None,
@@ -105,28 +118,26 @@ def paged_attention(q, k_pages, v_pages, table, lengths, *, softcap=0.0, slopes=
     lengths - 1); weights, if given, gain each slot's softmax weight, summed over the query
     heads of its key head.
     """
-    dt, n_seq, n_pages, page, width, hk, d = _pools(k_pages, v_pages, table, lengths)
-    if q.dim() != 3:
-        raise ValueError("q must be [n_seq][heads][head_dim]")
-    h = q.shape[1]
-    _need(q, k_pages.dtype, "q", (n_seq, h, d))
-    _here(q, "q")
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _need(out, q.dtype, "out", q.shape)
-        _here(out, "out")
-    cap = _capacity(positions, weights, n_seq, hk)
-    tokens = min(width * page, cap) if cap else width * page
-    need = L.lib.sfm_paged_attention_workspace_bytes(n_seq, tokens, h, hk, d, dt, weights is not None)
-    ws = _scratch(workspace, need, q.device)
-    L.check(L.lib.sfm_paged_attention(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-        out.data_ptr(), n_seq, n_pages, page, width, h, hk, d, dt, softcap or 0.0,
-        _opt(slopes, torch.float32, "slopes", (h,)), _opt(positions, torch.int32, "positions", None),
-        _opt(q_positions, torch.int32, "q_positions", (n_seq,)),
-        _opt(weights, torch.float32, "weights", None), cap, ws.data_ptr() if ws is not None else 0,
-        ws.numel() * ws.element_size() if ws is not None else 0, _raw_stream()), "sfm_paged_attention")
+    dev = torch.cuda.current_device()
+    n_pages, page, hk, d = pool = _dims(k_pages, 4, "k_pages", _POOL)
+    dt = k_pages.dtype
+    n_seq, width = _width(table)
+    h = _dims(q, 3, "q", "[n_seq][heads][head_dim]")[1]
+    pq = _ptr(q, dt, "q", (n_seq, h, d), dev)
+    cap, pos, wts = _capacity(positions, weights, n_seq, hk, dev)
+    args = (pq, _ptr(k_pages, dt, "k_pages", pool, dev), _ptr(v_pages, dt, "v_pages", pool, dev),
+            _ptr(table, _I32, "table", (n_seq, width), dev), _ptr(lengths, _I32, "lengths", (n_seq,), dev))
+    slp = _opt(slopes, _F32, "slopes", (h,), dev)
+    qpos = _opt(q_positions, _I32, "q_positions", (n_seq,), dev)
+    out = _result(out, q, dev)
+    tokens = width * page
+    if cap and cap < tokens:
+        tokens = cap
+    ws, wp, wb = _scratch(workspace, _attention_bytes(n_seq, tokens, h, hk, d, _DT[dt], int(weights is not None)),
+                          dev)
+    L.check(L.lib.sfm_paged_attention(*args, out.data_ptr(), n_seq, n_pages, page, width, h, hk, d, _DT[dt],
+                                      softcap or 0.0, slp, pos, qpos, wts, cap, wp, wb, _raw_stream(dev)),
+            "sfm_paged_attention")
     return out
 
 
@@ -138,18 +149,18 @@ def paged_evict(k_pages, v_pages, table, lengths, weights, positions, keep, *, n
     weights (ties: the lower slot).  Kept rows behind slot `keep` move into the evicted slots
     before it.  `lengths` is not changed; the new ones are lengths.clamp(max=keep).
     """
-    dt, n_seq, n_pages, page, width, hk, d = _pools(k_pages, v_pages, table, lengths)
+    dev = torch.cuda.current_device()
+    n_pages, page, hk, d = pool = _dims(k_pages, 4, "k_pages", _POOL)
+    dt = k_pages.dtype
+    n_seq, width = _width(table)
     if weights is None or positions is None:
         raise ValueError("paged_evict needs weights and positions")
-    cap = _capacity(positions, weights, n_seq, hk)
-    need = L.lib.sfm_paged_evict_workspace_bytes(n_seq, min(width * page, cap), hk, keep)
-    ws = _scratch(workspace, need, k_pages.device)
-    L.check(L.lib.sfm_paged_evict(
-        k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-        _opt(weights, torch.float32, "weights", None), _opt(positions, torch.int32, "positions", None), cap,
-        n_seq, n_pages, page, width, hk, d, dt, keep, n_first, n_recent,
-        ws.data_ptr() if ws is not None else 0, ws.numel() * ws.element_size() if ws is not None else 0,
-        _raw_stream()), "sfm_paged_evict")
+    cap, pos, wts = _capacity(positions, weights, n_seq, hk, dev)
+    args = (_ptr(k_pages, dt, "k_pages", pool, dev), _ptr(v_pages, dt, "v_pages", pool, dev),
+            _ptr(table, _I32, "table", (n_seq, width), dev), _ptr(lengths, _I32, "lengths", (n_seq,), dev))
+    ws, wp, wb = _scratch(workspace, _evict_bytes(n_seq, min(width * page, cap), hk, keep), dev)
+    L.check(L.lib.sfm_paged_evict(*args, wts, pos, cap, n_seq, n_pages, page, width, hk, d, _DT[dt], keep,
+                                  n_first, n_recent, wp, wb, _raw_stream(dev)), "sfm_paged_evict")
 
 
 def attention_bounds(n_q, n_kv, *, doc_starts=None, prefixes=None, causal=False, out=None):
@@ -159,13 +170,13 @@ def attention_bounds(n_q, n_kv, *, doc_starts=None, prefixes=None, causal=False,
     document of all); a query sees its own document, or (causal) its keys up to the query's own
     and its first prefixes[d].  Queries in no document get an empty range.
     """
-    dev = torch.device("cuda", torch.cuda.current_device())
+    dev = torch.cuda.current_device()
     n_docs = doc_starts.numel() - 1 if doc_starts is not None else (1 if prefixes is not None else 0)
-    lo, hi = out if out is not None else torch.empty((2, n_q), dtype=torch.int32, device=dev)
+    lo, hi = torch.empty((2, n_q), dtype=_I32, device=dev).unbind() if out is None else out
     L.check(L.lib.sfm_attention_bounds(
-        n_q, n_kv, _opt(doc_starts, torch.int32, "doc_starts", (n_docs + 1,)),
-        _opt(prefixes, torch.int32, "prefixes", (n_docs,)), n_docs, 1 if causal else 0,
-        _opt(lo, torch.int32, "lo", (n_q,)), _opt(hi, torch.int32, "hi", (n_q,)), _raw_stream()),
+        n_q, n_kv, _opt(doc_starts, _I32, "doc_starts", (n_docs + 1,), dev),
+        _opt(prefixes, _I32, "prefixes", (n_docs,), dev), n_docs, 1 if causal else 0,
+        _ptr(lo, _I32, "lo", (n_q,), dev), _ptr(hi, _I32, "hi", (n_q,), dev), _raw_stream(dev)),
         "sfm_attention_bounds")
     return lo, hi
 
@@ -177,27 +188,16 @@ def attention_masked(q, k, v, key_lo=None, key_hi=None, *, softcap=0.0, slopes=N
 
     softcap > 0 caps the scores; slopes ([heads] fp32) subtract slope |n_kv - n_q + i - j|.
     """
-    dt = _dtype(q, "q")
-    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("q must be [n_q][heads][D] and k [n_kv][kv_heads][D]")
-    n_q, h, d = q.shape
-    n_kv, hk = k.shape[0], k.shape[1]
-    _need(q, q.dtype, "q")
-    _need(k, q.dtype, "k", (n_kv, hk, d))
-    _need(v, q.dtype, "v", k.shape)
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _here(t, name)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _need(out, q.dtype, "out", q.shape)
-        _here(out, "out")
-    need = L.lib.sfm_attention_masked_workspace_bytes(n_q, n_kv, h, hk, d, dt)
-    ws = _scratch(workspace, need, q.device)
-    L.check(L.lib.sfm_attention_masked(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), n_q, n_kv, h, hk, d, dt,
-        _opt(key_lo, torch.int32, "key_lo", (n_q,)), _opt(key_hi, torch.int32, "key_hi", (n_q,)),
-        softcap or 0.0, _opt(slopes, torch.float32, "slopes", (h,)),
-        ws.data_ptr() if ws is not None else 0, ws.numel() * ws.element_size() if ws is not None else 0,
-        _raw_stream()), "sfm_attention_masked")
+    dev = torch.cuda.current_device()
+    n_q, h, d = shape = _dims(q, 3, "q", "[n_q][heads][D]")
+    n_kv, hk, _ = _dims(k, 3, "k", "[n_kv][kv_heads][D]")
+    dt = q.dtype
+    args = (_ptr(q, dt, "q", shape, dev), _ptr(k, dt, "k", (n_kv, hk, d), dev), _ptr(v, dt, "v", (n_kv, hk, d), dev))
+    lo = _opt(key_lo, _I32, "key_lo", (n_q,), dev)
+    hi = _opt(key_hi, _I32, "key_hi", (n_q,), dev)
+    slp = _opt(slopes, _F32, "slopes", (h,), dev)
+    out = _result(out, q, dev)
+    ws, wp, wb = _scratch(workspace, _masked_bytes(n_q, n_kv, h, hk, d, _DT[dt]), dev)
+    L.check(L.lib.sfm_attention_masked(*args, out.data_ptr(), n_q, n_kv, h, hk, d, _DT[dt], lo, hi,
+                                       softcap or 0.0, slp, wp, wb, _raw_stream(dev)), "sfm_attention_masked")
     return out
