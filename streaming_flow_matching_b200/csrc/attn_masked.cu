@@ -14,8 +14,8 @@
 //               tiles in a 2-stage ring (128-byte swizzle)
 //   warp 1      TMEM allocator; one lane issues S_t = Q_t K_j^T and O_t += P_t V_j (P from
 //               TMEM), alternating the tiles
-//   warps 4-11  softmax, thread = query row: one pass over S computes P against the
-//               running max, which moves only when a score passes it by 2^8
+//   warps 4-11  softmax, thread = query row: a look at the largest product, then P against
+//               the running max, which moves only when a score passes it by 2^8
 //   warp 2      makes V safe: a masked key has weight 0, and 0 x inf or 0 x NaN would
 //               still reach rows that may not see it.  In key tiles that some row does not
 //               see whole it scans V and replaces non-finite elements by 0; if it found
@@ -509,29 +509,90 @@ __global__ void __launch_bounds__(THREADS, 1)
         break;
       }
       tc_fence_after();
-      uint32_t pk[4][16];
       if (nothing) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int i = 0; i < 16; ++i) pk[i] = 0u;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) pk[c][i] = 0u;
+        for (int c = 0; c < 4; ++c) tmem_st16(tmem + lane_base + col_s + c * 16, pk);
       } else {
-        // P = 2^(z - m) of the 128 columns; masked ones give 0.  Returns the row's sum.
-        // Where the warp's rows lie on one side of the keys the bias is linear in the column
-        // (|slope fq| is kept below 2^14, so that the sum rounds at 2^-10 at most).
+        // The row's max may stay where it is while no score passes it by 2^8: first a bound
+        // from the largest product (magnitude, with a cap) and the largest bias of the tile,
+        // and only if that does not settle it the scores' own maximum.
+        float top = CAP ? 0.f : -INFINITY;
+        {
+          uint32_t u[2][32];
+          tmem_ld32(tmem + lane_base + col_s, u[0]);
+          tmem_wait_ld(u[0]);
+          float m4[4] = {top, top, top, top};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c + 1 < 4) tmem_ld32(tmem + lane_base + col_s + (c + 1) * 32, u[(c + 1) & 1]);
+            const float* sv = reinterpret_cast<const float*>(u[c & 1]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              m4[(i >> 1) & 3] = CAP ? fmax3(m4[(i >> 1) & 3], fabsf(sv[i]), fabsf(sv[i + 1]))
+                                     : fmax3(m4[(i >> 1) & 3], sv[i], sv[i + 1]);
+            if (c + 1 < 4) tmem_wait_ld(u[(c + 1) & 1]);
+          }
+          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        }
+        float bound = CAP ? sm.cap2 * fminf(top * sm.sc, 1.f) : top * sm.sc;
+        if (BIAS) {
+          const float d0 = fabsf(fq), d1 = fabsf(fq - (float)(BKV - 1));
+          const bool inside = fq >= 0.f && fq <= (float)(BKV - 1);
+          bound -= sm.slope2 * (sm.slope2 < 0.f ? fmaxf(d0, d1) : inside ? 0.f : fminf(d0, d1));
+        }
+        if (__any_sync(0xffffffffu, !(bound <= m + kRescaleLog2))) {
+          float mx = -INFINITY;                                // of the visible scores
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[16];
+            tmem_ld16(tmem + lane_base + col_s + c * 16, w);
+            tmem_wait_ld(w);
+            const float* sv = reinterpret_cast<const float*>(w);
+            const uint32_t bits = range_bits(lo - c * 16, hi - c * 16);
+            const float fc = fq - (float)(c * 16);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float z = score2<CAP, BIAS>(sm, sv[i], fc, (float)i);
+              if ((bits >> i) & 1u) mx = fmaxf(mx, z);
+            }
+          }
+          if (__any_sync(0xffffffffu, mx > m + kRescaleLog2)) {   // also from m = -inf
+            const float m_new = fmaxf(m, mx);
+            const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);   // O, l are 0 then
+            l *= alpha;
+            m = m_new;
+            if (j > 0) {
+              // O_t's previous P V has completed (S_t(j) was issued after it): rescale it
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lane_base + col_o + c * 32, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st32(tmem + lane_base + col_o + c * 32, o);
+              }
+            }
+          }
+        }
+        // P = 2^(z - m) of the 128 columns, written over S as packed bf16 as it is made (the
+        // 16 columns a chunk of 32 becomes have been read); masked columns give 0.
+        // FAST: the bias linear in the column, as where the warp's rows lie on one side of the
+        // keys (|slope fq| kept below 2^14: the sum then rounds at 2^-10 at most), and the cap
+        // by its polynomial; else the general forms.
         const float side = key0 + BKV - 1 <= w_pos0 ? 1.f : key0 >= w_pos1 ? -1.f : 0.f;
-        const bool linear =
-            !BIAS || (side != 0.f && __all_sync(0xffffffffu, fabsf(sm.slope2 * fq) < 16384.f));
-        // FAST: the bias linear, the cap by polynomial (x_top then holds the row's largest |x|:
-        // past x_lim the result does not stand); else the general form.
-        float x_top = 0.f;
-        auto attempt = [&](float neg_m, auto is_masked, auto is_fast) -> float {
+        bool fast = true;
+        if (BIAS) fast = side != 0.f && __all_sync(0xffffffffu, fabsf(sm.slope2 * fq) < 16384.f);
+        if (CAP) fast = fast && __all_sync(0xffffffffu, top <= sm.x_lim);
+        auto make_p = [&](auto is_masked, auto is_fast) {
           constexpr bool MASKED = decltype(is_masked)::value, FAST = decltype(is_fast)::value;
           F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
-          float tilt = sm.slope2 * side, fql = fq;             // z gains tilt (col - fq)
-          asm volatile("" : "+f"(tilt), "+f"(fql));            // 128 columns' terms are not worth keeping
-          const float t0 = BIAS && FAST ? fmaf(-tilt, fql, neg_m) : neg_m;
-          if (CAP && FAST) x_top = 0.f;
+          const float neg_m = m == -INFINITY ? 0.f : -m;
+          const float tilt = sm.slope2 * side;                 // z gains tilt (col - fq)
+          const float t0 = BIAS && FAST ? fmaf(-tilt, fq, neg_m) : neg_m;
           uint32_t u[2][32];
           tmem_ld32(tmem + lane_base + col_s, u[0]);
           tmem_wait_ld(u[0]);
@@ -540,13 +601,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (c + 1 < 4) tmem_ld32(tmem + lane_base + col_s + (c + 1) * 32, u[(c + 1) & 1]);
             const float* sv = reinterpret_cast<const float*>(u[c & 1]);
             const uint32_t bits = MASKED ? range_bits(lo - c * 32, hi - c * 32) : 0u;
+            uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               F2 t(t0, t0);
               if (BIAS) {
                 const float c0 = (float)(c * 32 + 2 * i), c1 = c0 + 1.f;
                 t = FAST ? F2(fmaf(tilt, c0, t0), fmaf(tilt, c1, t0))
-                         : F2(fmaf(-sm.slope2, fabsf(fql - c0), t0), fmaf(-sm.slope2, fabsf(fql - c1), t0));
+                         : F2(fmaf(-sm.slope2, fabsf(fq - c0), t0), fmaf(-sm.slope2, fabsf(fq - c1), t0));
               }
               const float x0 = sv[2 * i], x1 = sv[2 * i + 1];
               const F2 x(x0, x1);
@@ -554,7 +616,6 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (!CAP) {
                 z = fma2(x, sc2, t);
               } else if (FAST) {
-                x_top = fmax3(x_top, fabsf(x0), fabsf(x1));
                 const F2 y2 = mul2(x, x);
                 F2 w = poly[4];
 #pragma unroll
@@ -572,75 +633,19 @@ __global__ void __launch_bounds__(THREADS, 1)
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
               sum[i & 1] = add2(sum[i & 1], F2(p0, p1));
-              pk[c][i] = pack_bf16x2(p0, p1);
+              pk[i] = pack_bf16x2(p0, p1);
             }
             if (c + 1 < 4) tmem_wait_ld(u[(c + 1) & 1]);
+            tmem_st16(tmem + lane_base + col_s + c * 16, pk);
           }
           float a0, a1;
           add2(sum[0], sum[1]).get(&a0, &a1);
-          return a0 + a1;
+          l += a0 + a1;
         };
-        auto row_max = [&]() -> float {                        // of the visible scores
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t w[16];
-            tmem_ld16(tmem + lane_base + col_s + c * 16, w);
-            tmem_wait_ld(w);
-            const float* sv = reinterpret_cast<const float*>(w);
-            const uint32_t bits = range_bits(lo - c * 16, hi - c * 16);
-            const float fc = fq - (float)(c * 16);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float z = score2<CAP, BIAS>(sm, sv[i], fc, (float)i);
-              if ((bits >> i) & 1u) mx = fmaxf(mx, z);
-            }
-          }
-          return mx;
-        };
-        float lt = 0.f;
-        // a warp none of whose rows has a max yet takes it first
-        bool done = !__all_sync(0xffffffffu, m == -INFINITY);
-        for (int round = done ? 0 : 1; round < 3; ++round) {
-          if (round != 1) {
-            const float neg_m = m == -INFINITY ? 0.f : -m;
-            bool general = !linear;
-            if (linear) {
-              lt = masked ? attempt(neg_m, Yes{}, Yes{}) : attempt(neg_m, No{}, Yes{});
-              if (CAP) general = __any_sync(0xffffffffu, !(x_top <= sm.x_lim));
-            }
-            if ((CAP || BIAS) && general) lt = attempt(neg_m, Yes{}, No{});
-            // a score can only have passed the max by 2^8 if the row's sum did
-            if (round == 2 || !__any_sync(0xffffffffu, m == -INFINITY || !(lt <= 256.f))) break;
-          } else {
-            const float mx = row_max();
-            const bool grown = mx > m + kRescaleLog2;          // also from m = -inf
-            if (__any_sync(0xffffffffu, grown)) {
-              const float m_new = fmaxf(m, mx);
-              const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);   // O, l are 0 then
-              l *= alpha;
-              m = m_new;
-              if (j > 0) {
-                // O_t's previous P V has completed (S_t(j) was issued after it): rescale it
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  uint32_t o[32];
-                  tmem_ld32(tmem + lane_base + col_o + c * 32, o);
-                  tmem_wait_ld(o);
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                  tmem_st32(tmem + lane_base + col_o + c * 32, o);
-                }
-              }
-            } else if (done) {
-              break;                                           // the first attempt stands
-            }
-          }
-        }
-        l += lt;
+        if (fast && !masked) make_p(No{}, Yes{});
+        else if (fast) make_p(Yes{}, Yes{});
+        else if (CAP || BIAS) make_p(Yes{}, No{});
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_st16(tmem + lane_base + col_s + c * 16, pk[c]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
