@@ -248,8 +248,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch(&map_q);
+  // the Q tiles do not wait for the ranges (the barrier's own initialising thread loads them)
+  const bool loads = !(args.fault & SFM_FAULT_ATTN_NO_LOADS);
+  if (threadIdx.x == 0) {
+    if (loads) {
+      mbar_arrive_expect_tx(q_full, QT * TILE);
+      for (int t = 0; t < QT; ++t) {
+        tma_load_3d(base + OFF_Q + t * TILE, &map_q, q_full, 0, h_a + t * dh, row0 + t * dr);
+        tma_load_3d(base + OFF_Q + t * TILE + HALF, &map_q, q_full, 64, h_a + t * dh, row0 + t * dr);
+      }
+    }
     tma_prefetch(&map_k);
     tma_prefetch(&map_v);
   }
@@ -317,17 +325,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0 && T > 0 && !(args.fault & SFM_FAULT_ATTN_NO_LOADS)) {
+    if (lane == 0 && T == 0 && loads) mbar_drain(q_full, 0, args.wait_ns);   // nothing else waits for Q
+    if (lane == 0 && T > 0 && loads) {
       // ---------------- TMA producer ----------------
       int kp[KST], vp[VST];
       for (int i = 0; i < KST; ++i) kp[i] = -1;
       for (int i = 0; i < VST; ++i) vp[i] = -1;
       bool ok = true;
-      mbar_arrive_expect_tx(q_full, QT * TILE);
-      for (int t = 0; t < QT; ++t) {
-        tma_load_3d(base + OFF_Q + t * TILE, &map_q, q_full, 0, h_a + t * dh, row0 + t * dr);
-        tma_load_3d(base + OFF_Q + t * TILE + HALF, &map_q, q_full, 64, h_a + t * dh, row0 + t * dr);
-      }
       auto load_k = [&](int i) -> bool {
         const int s = i % KST;
         const uint32_t par = (uint32_t)((i / KST) & 1);
@@ -545,6 +549,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (__any_sync(0xffffffffu, !(bound <= m + kRescaleLog2))) {
           float mx = -INFINITY;                                // of the visible scores
+          // With nothing masked and no bias the bound is itself the largest score, or (cap) as
+          // far above it that no score is lost under 2^-126 while it is small.
+          if (!BIAS && !masked && __all_sync(0xffffffffu, !CAP || bound <= 40.f)) mx = bound;
+          else
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t w[16];
