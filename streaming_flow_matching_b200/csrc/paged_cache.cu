@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kHeldRanks = 48 * 1024;   // ranks in shared memory: 192 KB
 
 // Rank of a token as an unsigned number, larger = kept first: NaN below every number,
 // -0 equal to +0, protected tokens above all.
@@ -107,13 +108,17 @@ __device__ __forceinline__ int warp_sum(int v) {
 }
 
 // lists: per (sequence, key head) `room` evicted slots then `room` moved slots; counts: one each.
+// The ranks are made once and kept in shared memory (`held` of them at most; a longer
+// sequence makes them again in each of the five passes): 36,000 slots took 90 us when every
+// pass read weights and positions from L2.
 __global__ void __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictArgs a, int* __restrict__ counts,
-                        int* __restrict__ lists, int room) {
+                        int* __restrict__ lists, int room, int held) {
+  extern __shared__ unsigned ranks[];
   __shared__ unsigned hist[kBins];
   __shared__ int part[3][kSelWarps];
   __shared__ unsigned sh_digit;
-  __shared__ int sh_above, sh_max;
+  __shared__ int sh_above;
   const int item = blockIdx.x, seq = item / a.c.kv_heads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = cache_len(a.c, seq, a.err), keep = a.keep;
@@ -125,14 +130,21 @@ __global__ void __launch_bounds__(kSelThreads)
   const int* pos = a.positions + (size_t)item * a.cap;
   // newest position
   int mx = INT_MIN;
-  for (int t = tid; t < n; t += kSelThreads) mx = max(mx, pos[t]);
-  if (tid == 0) sh_max = INT_MIN;
-  __syncthreads();
+#pragma unroll 8
+  for (int t = tid; t < n; t += kSelThreads) mx = max(mx, __ldg(pos + t));
   mx = __reduce_max_sync(0xffffffffu, mx);
-  if (lane == 0) atomicMax(&sh_max, mx);
+  if (lane == 0) part[0][warp] = mx;
   __syncthreads();
-  const long long recent_from = (long long)sh_max - a.n_recent + 1;
-  auto rank = [&](int t) { return rank_of(w[t], pos[t], a.n_first, recent_from); };
+  mx = __reduce_max_sync(0xffffffffu, part[0][lane]);
+  __syncthreads();
+  const long long recent_from = (long long)mx - a.n_recent + 1;
+  const bool hold = n <= held;
+  auto make_rank = [&](int t) { return rank_of(__ldg(w + t), __ldg(pos + t), a.n_first, recent_from); };
+  if (hold) {
+#pragma unroll 8
+    for (int t = tid; t < n; t += kSelThreads) ranks[t] = make_rank(t);
+  }
+  auto rank = [&](int t) { return hold ? ranks[t] : make_rank(t); };
   // the keep-th largest rank, digit by digit: `want` of the ranks that match the
   // prefix found so far are still to be taken
   unsigned prefix = 0, mask = 0;
@@ -142,6 +154,7 @@ __global__ void __launch_bounds__(kSelThreads)
     const unsigned bins = d == 2 ? 1024u : 2048u;
     for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int t = tid; t < n; t += kSelThreads) {
       const unsigned r = rank(t);
       if ((r & mask) == prefix) atomicAdd(&hist[(r >> shift) & (bins - 1)], 1u);
@@ -178,6 +191,7 @@ __global__ void __launch_bounds__(kSelThreads)
   const int per = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
   const int t0 = min(n, warp * per), t1 = min(n, t0 + per);
   int ties = 0;
+#pragma unroll 4
   for (int t = t0 + lane; t < t1; t += 32) ties += rank(t) == prefix;
   ties = warp_sum(ties);
   if (lane == 0) part[0][warp] = ties;
@@ -224,9 +238,11 @@ __global__ void __launch_bounds__(kSelThreads)
   }
 }
 
-constexpr int kMoveWarps = 8;
+// A warp moves kMoveRows rows at a time: their slots and pages are looked up by as many
+// lanes at once, then the 16-byte pieces of all of them (head_vecs of K and of V each) are
+// loaded four to a lane before the first is stored.
+constexpr int kMoveWarps = 8, kMoveRows = 8;
 
-// head_vecs: 16-byte pieces of one head's row
 __global__ void __launch_bounds__(kMoveWarps * 32)
     evict_move_kernel(const __grid_constant__ EvictArgs a, const int* __restrict__ counts,
                       const int* __restrict__ lists, int room, int head_vecs, int blocks_per_item) {
@@ -237,22 +253,38 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
   const int n = counts[item];
   const int* outs = lists + (size_t)item * 2 * room;
   const int* mvs = outs + room;
-  for (int i = blk * kMoveWarps + (threadIdx.x >> 5); i < n; i += blocks_per_item * kMoveWarps) {
-    const int to = outs[i], from = mvs[i];
-    const int rt = cache_row(a.c, seq, to, a.err), rf = cache_row(a.c, seq, from, a.err);
-    if (rt >= 0 && rf >= 0) {
-      const size_t dst = ((size_t)rt * a.c.kv_heads + h) * head_vecs;
-      const size_t src = ((size_t)rf * a.c.kv_heads + h) * head_vecs;
-      for (int x = lane; x < 2 * head_vecs; x += 32) {
-        uint4* p = reinterpret_cast<uint4*>(x < head_vecs ? a.k_pages : a.v_pages);
-        const int c = x < head_vecs ? x : x - head_vecs;
-        p[dst + c] = p[src + c];
-      }
-    }
-    if (lane == 0) {
+  const int pieces = 2 * head_vecs;                            // of a row; kMoveRows * pieces is a multiple of 128
+  uint4* kp = reinterpret_cast<uint4*>(a.k_pages);
+  uint4* vp = reinterpret_cast<uint4*>(a.v_pages);
+  for (int i0 = (blk * kMoveWarps + (threadIdx.x >> 5)) * kMoveRows; i0 < n;
+       i0 += blocks_per_item * kMoveWarps * kMoveRows) {
+    int rt = -1, rf = -1;
+    if (lane < kMoveRows && i0 + lane < n) {
+      const int to = outs[i0 + lane], from = mvs[i0 + lane];
+      rt = cache_row(a.c, seq, to, a.err);
+      rf = cache_row(a.c, seq, from, a.err);
       const size_t at = (size_t)item * a.cap;
       a.weights[at + to] = a.weights[at + from];
       a.positions[at + to] = a.positions[at + from];
+    }
+    for (int x0 = lane; x0 < kMoveRows * pieces; x0 += 128) {
+      uint4 d[4];
+      uint4* to[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int x = x0 + 32 * u, r = x / pieces, c = x - r * pieces;
+        const int from_row = __shfl_sync(0xffffffffu, rf, r), to_row = __shfl_sync(0xffffffffu, rt, r);
+        uint4* pool = c < head_vecs ? kp : vp;
+        const int cc = c < head_vecs ? c : c - head_vecs;
+        to[u] = nullptr;
+        if (from_row >= 0 && to_row >= 0) {
+          d[u] = pool[((size_t)from_row * a.c.kv_heads + h) * head_vecs + cc];
+          to[u] = pool + ((size_t)to_row * a.c.kv_heads + h) * head_vecs + cc;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (to[u]) *to[u] = d[u];
     }
   }
 }
@@ -289,12 +321,16 @@ int launch_paged_evict(const EvictArgs& a, int row_bytes_head, void* workspace, 
   int* counts = (int*)workspace;
   int* lists = counts + items;
   ProfScope ps(SFM_PROF_APPEND, s);
-  evict_select_kernel<<<(unsigned)items, kSelThreads, 0, s>>>(a, counts, lists, room);
+  const int held = a.c.max_tokens < kHeldRanks ? a.c.max_tokens : kHeldRanks;
+  const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kHeldRanks * (int)sizeof(unsigned));
+  if (e != cudaSuccess) return record_cuda(e);
+  evict_select_kernel<<<(unsigned)items, kSelThreads, held * sizeof(unsigned), s>>>(a, counts, lists, room, held);
   int rc = record_cuda(cudaGetLastError());
   if (rc) return rc;
-  // a few rows per warp, and no more CTAs than fill the device several times over
-  int blocks = (room + 4 * kMoveWarps - 1) / (4 * kMoveWarps);
-  const int most = (148 * 16 + items - 1) / items;
+  // kMoveRows rows per warp, and no more CTAs than fill the device several times over
+  int blocks = (room + kMoveRows * kMoveWarps - 1) / (kMoveRows * kMoveWarps);
+  const int most = (148 * 32 + items - 1) / items;
   if (blocks > most) blocks = most;
   return record_cuda(launch_dependent(evict_move_kernel, (unsigned)(items * blocks), kMoveWarps * 32, 0, s, a,
                                       (const int*)counts, (const int*)lists, room, row_bytes_head / 16, blocks));
