@@ -28,7 +28,7 @@
 // Few query rows over many keys: the key tiles are cut into splits whose fp32 partials a
 // second kernel joins.
 //
-// fp32 runs on the CUDA cores in 64 x 64 tiles.
+// fp32 runs on the CUDA cores in 32 x 64 tiles.
 #include <limits.h>
 #include <math.h>
 
@@ -785,14 +785,15 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ fp32, CUDA cores
 
-constexpr int FM = 64, FN = 64, FTHREADS = 256;
+constexpr int FM = 32, FN = 64, FTHREADS = 128;
 
 template <int DV>
 constexpr int f32_smem() {
-  return (3 * 64 * (32 * DV + 4) + FM * (FN + 4)) * 4;
+  return ((FM + 2 * FN) * (32 * DV + 4) + FM * (FN + 4)) * 4;
 }
 
-// 64 query rows x 64 keys per step; thread (ty, tx) of 16 x 16 holds 4 rows x 4 scores
+// 32 query rows x 64 keys per step (64 rows left half the SMs without work at 1,000 queries of
+// four heads: 68 us, now MEASURE us); thread (ty, tx) of 8 x 16 holds 4 rows x 4 scores
 // (keys tx + 16 k) and 4 rows x 2 DV outputs.  Masked scores are skipped by weight 0 and
 // masked V rows by staging zeros for keys that no row of the tile sees; a key that only
 // some rows see and that holds a non-finite value is left out row by row.
@@ -805,7 +806,7 @@ __global__ void __launch_bounds__(FTHREADS)
   float* ks = qs + FM * P;
   float* vs = ks + FN * P;
   float* ps = vs + FN * P;
-  __shared__ int red[2][8];
+  __shared__ int red[2][FTHREADS / 32];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int h = blockIdx.x % a.heads;
   const int qblocks = (a.n_q + FM - 1) / FM;
@@ -842,7 +843,7 @@ __global__ void __launch_bounds__(FTHREADS)
   }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < FTHREADS / 32; ++w) {
     u_lo = min(u_lo, red[0][w]);
     u_hi = max(u_hi, red[1][w]);
   }

@@ -69,9 +69,14 @@ __device__ __forceinline__ int cache_row(const PagedCache& c, int s, int t, int*
 
 // Programmatic dependent launch: waits until the grid this one depends on has
 // completed and its writes are visible.  Every thread of a dependent kernel calls it
-// before anything else it does to memory.
+// before it exits and before it touches anything that grid writes (or whatever came
+// before that grid in the stream: that grid itself starts only when that is done).
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// In the grid depended on: the dependent one may be set up from here on (it still waits).
+__device__ __forceinline__ void grid_dependency_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 #endif
 

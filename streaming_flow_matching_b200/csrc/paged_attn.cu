@@ -50,7 +50,9 @@ struct Split {
   float* part;          // [slots][hgroups][2][hpt][D]
   float* ml;            // [slots][hgroups][2][hpt][2]: running max (log2), sum
   float* lse;           // [n_seq][H] (log2; with weights)
-  float* scores;        // [n_seq][H][max_tokens] (log2; with weights)
+  float* scores;        // [n_seq][H][pitch] (log2; with weights)
+  int pitch;            // max_tokens
+  int joins;            // CTAs of the finishing kernel that join, before those that add weights
 };
 
 // Number of tiles of all sequences, by one warp.
@@ -174,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int g0 = (hg - hk * sp.gt) * (8 * NT);                // first query head of the group here
   const int nh = min(8 * NT, G - g0);                         // query heads of this tile
   const int h0 = hk * G + g0;
+  grid_dependency_trigger();                                  // the finishing kernel may be set up
   const int total = total_tiles(a.c, lane, a.err);
   const int chunk = (total + sp.slots - 1) / sp.slots;
   const int b0 = slot * chunk, b1 = min(total, b0 + chunk);
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int e = 0; e < 4; ++e) {
             const int hh = nt * 8 + 2 * t4 + (e & 1), tt = tok + (e >= 2 ? 8 : 0);
             if (hh < nh && tt < cw.len)
-              sp.scores[((size_t)cw.seq * a.heads + h0 + hh) * a.c.max_tokens + tt] = s[nt][e];
+              sp.scores[((size_t)cw.seq * a.heads + h0 + hh) * sp.pitch + tt] = s[nt][e];
           }
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -467,6 +470,7 @@ __global__ void __launch_bounds__(kThreads)
   const int g0 = (hg - hk * sp.gt) * GT;
   const int nh = min(GT, G - g0);
   const int h0 = hk * G + g0;
+  grid_dependency_trigger();                                  // the finishing kernel may be set up
   const int total = total_tiles(a.c, lane, a.err);
   const int chunk = (total + sp.slots - 1) / sp.slots;
   const int b0 = slot * chunk, b1 = min(total, b0 + chunk);
@@ -480,6 +484,26 @@ __global__ void __launch_bounds__(kThreads)
   const float scale = rsqrtf((float)D);
   const bool cap = a.softcap > 0.f;
   const float inv_cap = cap ? 1.f / a.softcap : 0.f;
+
+  // pool row of this lane's token (lanes 0..15) of a tile; -1: none
+  auto lookup = [&](const Walk& w) -> int {
+    const int t = w.tile * kTile + warp * kWarpTok + lane;
+    return lane < kWarpTok && t < w.len ? cache_row(a.c, w.seq, t, a.err) : -1;
+  };
+  float4 kn[DV], vn[DV];
+  auto load_rows = [&](int row) {
+#pragma unroll
+    for (int i = 0; i < DV; ++i) {
+      kn[i] = vn[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row >= 0) {
+        kn[i] = __ldg(kp + (size_t)row * row_vecs + j + 8 * i);
+        vn[i] = __ldg(vp + (size_t)row * row_vecs + j + 8 * i);
+      }
+    }
+  };
+  int row16 = lookup(cw);
+  int row_now = __shfl_sync(0xffffffffu, row16, grp);
+  load_rows(row_now);
 
   float4 acc[GT][DV];
   float m[GT], l[GT], slope[GT];
@@ -507,21 +531,23 @@ __global__ void __launch_bounds__(kThreads)
       __syncthreads();
     }
     const int base = cw.tile * kTile + warp * kWarpTok;
-    int row16 = -1;
-    if (lane < kWarpTok && base + lane < cw.len) row16 = cache_row(a.c, cw.seq, base + lane, a.err);
+    Walk nw = cw;
+    nw.next(a.c);
+    const int next16 = b + 1 < b1 ? lookup(nw) : -1;
 #pragma unroll
     for (int step = 0; step < kWarpTok / 4; ++step) {
       const int tok = base + step * 4 + grp;
-      const int row = __shfl_sync(0xffffffffu, row16, step * 4 + grp);
+      // the rows of the step after this one are on their way while this one is computed
+      const int row = row_now;
       float4 kf[DV], vf[DV];
 #pragma unroll
       for (int i = 0; i < DV; ++i) {
-        kf[i] = vf[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row >= 0) {
-          kf[i] = __ldg(kp + (size_t)row * row_vecs + j + 8 * i);
-          vf[i] = __ldg(vp + (size_t)row * row_vecs + j + 8 * i);
-        }
+        kf[i] = kn[i];
+        vf[i] = vn[i];
       }
+      row_now = step + 1 < kWarpTok / 4 ? __shfl_sync(0xffffffffu, row16, (step + 1) * 4 + grp)
+                                        : __shfl_sync(0xffffffffu, next16, grp);
+      load_rows(row_now);
       float dist = 0.f;
       if (a.slopes && row >= 0) {
         const int p = a.positions ? __ldg(a.positions + ((size_t)cw.seq * a.c.kv_heads + hk) * a.cap + tok) : tok;
@@ -545,7 +571,7 @@ __global__ void __launch_bounds__(kThreads)
         else if (cap) s = finish_score<true>(s, scale, a.softcap, inv_cap, slope[hh], dist);
         else s = finish_score<false>(s, scale, 0.f, 0.f, slope[hh], dist);
         if (sp.scores && j == 0 && hh < nh && tok < cw.len)
-          sp.scores[((size_t)cw.seq * a.heads + h0 + hh) * a.c.max_tokens + tok] = s;
+          sp.scores[((size_t)cw.seq * a.heads + h0 + hh) * sp.pitch + tok] = s;
         if (__any_sync(0xffffffffu, s > m[hh] + kGrow)) {      // each group of 8 lanes has its own max
           const float mx = fmaxf(m[hh], s);
           const float al = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - mx);
@@ -570,6 +596,7 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
     }
+    row16 = next16;
     const int seq = cw.seq;
     const bool seq_done = (cw.tile + 1) * kTile >= cw.len;
     cw.next(a.c);
@@ -635,72 +662,158 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------------ join
 
-// One CTA per (sequence, query head): combines the sequence's partials in slot order;
-// a sequence finished by one CTA is left alone, an empty one gets zeros.
-template <typename T>
-__global__ void __launch_bounds__(128)
-    paged_join_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp) {
-  grid_dependency_wait();
-  const int seq = blockIdx.x / a.heads, h = blockIdx.x - seq * a.heads;
-  const int lane = threadIdx.x & 31, d = threadIdx.x, D = a.c.head_dim;
-  const int total = total_tiles(a.c, lane, nullptr);
-  int start = 0;
-  for (int s = lane; s < seq; s += 32) start += (cache_len(a.c, s, nullptr) + kTile - 1) / kTile;
+// Where a sequence's partials are: runs s0 .. s1 (one run: it was finished there), empty if
+// it has no tiles.
+struct Parts {
+  int nt, s0, s1;
+};
+
+__device__ Parts find_parts(const PagedCache& c, const Split& sp, int seq, int lane) {
+  int total = 0, start = 0;
+  for (int s = lane; s < c.n_seq; s += 32) {
+    const int nt = (cache_len(c, s, nullptr) + kTile - 1) / kTile;
+    total += nt;
+    start += s < seq ? nt : 0;
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) start += __shfl_xor_sync(0xffffffffu, start, o);
-  const int nt = (cache_len(a.c, seq, nullptr) + kTile - 1) / kTile;
-  T* out = reinterpret_cast<T*>(a.o) + ((size_t)seq * a.heads + h) * D;
-  if (nt == 0) {
-    if (d < D) out[d] = (T)0.f;
-    return;
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    start += __shfl_xor_sync(0xffffffffu, start, o);
+  }
+  Parts p;
+  p.nt = (cache_len(c, seq, nullptr) + kTile - 1) / kTile;
+  if (p.nt == 0) {
+    p.s0 = p.s1 = 0;
+    return p;
   }
   const int chunk = (total + sp.slots - 1) / sp.slots;
-  const int s0 = start / chunk, s1 = (start + nt - 1) / chunk;
-  if (s0 == s1) return;
-  const int G = a.heads / a.c.kv_heads;
-  const int hk = h / G, gi = h - hk * G;
-  const int hg = hk * sp.gt + gi / sp.hpt, ht = gi % sp.hpt;
-  // the run that holds tile 0 of the sequence wrote index 1, the later ones index 0
-  auto at = [&](int s) {
-    return (((size_t)s * sp.hgroups + hg) * 2 + (s == s0 ? 1 : 0)) * sp.hpt + ht;
-  };
-  float mm = -INFINITY;
-  for (int s = s0 + lane; s <= s1; s += 32) mm = fmaxf(mm, sp.ml[at(s) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-  const float mb = mm == -INFINITY ? 0.f : mm;
-  float sum = 0.f, acc = 0.f;
-#pragma unroll 4
-  for (int s = s0; s <= s1; ++s) {
-    const float f = ex2_approx(sp.ml[at(s) * 2] - mb);
-    sum = fmaf(f, sp.ml[at(s) * 2 + 1], sum);
-    if (d < D) acc = fmaf(f, sp.part[at(s) * D + d], acc);
-  }
-  if (d < D) out[d] = (T)(sum > 0.f || sum != sum ? acc / sum : 0.f);
-  if (sp.lse && d == 0) sp.lse[(size_t)seq * a.heads + h] = mb + log2f(sum);
+  p.s0 = start / chunk;
+  p.s1 = (start + p.nt - 1) / chunk;
+  return p;
 }
 
-// weights[seq][hk][t] += sum over the key head's query heads of 2^(score - lse).
-constexpr int kAccThreads = 256, kAccTok = 1024;
-__global__ void __launch_bounds__(kAccThreads)
-    paged_weights_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp, int blocks_per_item) {
-  grid_dependency_wait();
-  const int item = blockIdx.x / blocks_per_item, blk = blockIdx.x - item * blocks_per_item;
-  const int seq = item / a.c.kv_heads, hk = item - seq * a.c.kv_heads;
+// index of the partial of query head h in run s: the run that holds tile 0 of the sequence
+// wrote its second place, the later ones their first
+__device__ __forceinline__ size_t part_at(const Split& sp, int G, int h, int s, int s0) {
+  const int hk = h / G, gi = h - hk * G;
+  return (((size_t)s * sp.hgroups + hk * sp.gt + gi / sp.hpt) * 2 + (s == s0 ? 1 : 0)) * sp.hpt + gi % sp.hpt;
+}
+
+// max (log2) and sum of a head's partials, by one warp
+__device__ void join_ml(const Split& sp, int G, int h, const Parts& p, int lane, float* m, float* l) {
+  float mx = -INFINITY, sum = 0.f;
+  for (int s = p.s0 + lane; s <= p.s1; s += 32) mx = fmaxf(mx, sp.ml[part_at(sp, G, h, s, p.s0) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float mb = mx == -INFINITY ? 0.f : mx;
+  for (int s = p.s0 + lane; s <= p.s1; s += 32) {
+    const float2 v = *reinterpret_cast<const float2*>(sp.ml + part_at(sp, G, h, s, p.s0) * 2);
+    sum = fmaf(ex2_approx(v.x - mb), v.y, sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  *m = mb;
+  *l = sum;
+}
+
+constexpr int kFinThreads = 256, kFinWarps = kFinThreads / 32, kAccTok = 1024;
+
+// The finishing kernel.  Its first CTAs join, one per (sequence, query head): a sequence
+// finished by one CTA is left alone, an empty one gets zeros; the partials are summed in a
+// fixed order (float4 column x run, runs strided over the CTA, then over its groups).  The
+// others add weights, one per (sequence, key head, kAccTok slots): weights += sum over the
+// key head's query heads of 2^(score - lse).  Only the part that does not depend on the
+// attention kernel runs before the wait for it.
+template <typename T>
+__global__ void __launch_bounds__(kFinThreads)
+    paged_finish_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp, int blocks_per_item) {
+  __shared__ float4 buf[kFinThreads];
+  __shared__ float2 sh[kFinWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.heads / a.c.kv_heads;
+  if ((int)blockIdx.x < sp.joins) {
+    const int seq = blockIdx.x / a.heads, h = blockIdx.x - seq * a.heads, D = a.c.head_dim;
+    const Parts p = find_parts(a.c, sp, seq, lane);
+    grid_dependency_wait();
+    T* out = reinterpret_cast<T*>(a.o) + ((size_t)seq * a.heads + h) * D;
+    if (p.nt == 0) {
+      if (tid < D) out[tid] = (T)0.f;
+      return;
+    }
+    if (p.s0 == p.s1) return;
+    float mb, sum;
+    join_ml(sp, G, h, p, lane, &mb, &sum);                     // every warp the same
+    const int cols = D / 4, groups = kFinThreads / cols;       // 8, 16, 24 or 32 columns
+    const int c = tid % cols, g = tid / cols;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (g < groups) {
+#pragma unroll 4
+      for (int s = p.s0 + g; s <= p.s1; s += groups) {
+        const size_t at = part_at(sp, G, h, s, p.s0);
+        const float f = ex2_approx(sp.ml[at * 2] - mb);
+        const float4 v = *reinterpret_cast<const float4*>(sp.part + at * D + 4 * c);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+    }
+    buf[tid] = acc;
+    __syncthreads();
+    if (tid < D) {
+      float o = 0.f;
+      const int used = min(groups, p.s1 - p.s0 + 1);
+      for (int i = 0; i < used; ++i) o += reinterpret_cast<const float*>(buf + i * cols)[tid];
+      out[tid] = (T)(sum > 0.f || sum != sum ? o / sum : 0.f);
+    }
+    return;
+  }
+  const int b = blockIdx.x - sp.joins;
+  const int item = b / blocks_per_item, blk = b - item * blocks_per_item;
+  const int seq = item / a.c.kv_heads, hk = item - seq * a.c.kv_heads;
   const int n = cache_len(a.c, seq, nullptr);
   const int t1 = min(n, (blk + 1) * kAccTok);
-  const float* sc = sp.scores + ((size_t)seq * a.heads + hk * G) * a.c.max_tokens;
-  const float* lse = sp.lse + (size_t)seq * a.heads + hk * G;
+  if (blk * kAccTok >= t1) {
+    grid_dependency_wait();
+    return;
+  }
+  const Parts p = find_parts(a.c, sp, seq, lane);
+  grid_dependency_wait();
+  const float* sc = sp.scores + ((size_t)seq * a.heads + hk * G) * sp.pitch;
   float* w = a.weights + (size_t)item * a.cap;
-  for (int t = blk * kAccTok + threadIdx.x; t < t1; t += kAccThreads) {
-    float sum = 0.f;
-    for (int gi = 0; gi < G; ++gi) {
-      const float ls = __ldg(lse + gi);
-      // no visible token (every page bad): nothing to add
-      if (ls != -INFINITY) sum += ex2_approx(sc[(size_t)gi * a.c.max_tokens + t] - ls);
+  float add[kAccTok / kFinThreads];
+#pragma unroll
+  for (int i = 0; i < kAccTok / kFinThreads; ++i) add[i] = 0.f;
+  for (int g0 = 0; g0 < G; g0 += kFinWarps) {
+    if (g0 + warp < G) {
+      const int h = hk * G + g0 + warp;
+      float m, l;
+      if (p.s0 == p.s1) {                                      // the attention kernel left it whole
+        m = __ldcg(sp.lse + (size_t)seq * a.heads + h);
+        l = 1.f;
+      } else {
+        join_ml(sp, G, h, p, lane, &m, &l);
+        m += log2f(l);
+      }
+      if (lane == 0) sh[warp] = make_float2(m, l);
     }
-    w[t] += sum;
+    __syncthreads();
+    const int ng = min(kFinWarps, G - g0);
+    for (int gi = 0; gi < ng; ++gi) {
+      const float ls = sh[gi].x;
+      if (ls == -INFINITY) continue;                           // no visible slot (every page bad)
+#pragma unroll
+      for (int i = 0; i < kAccTok / kFinThreads; ++i) {
+        const int t = blk * kAccTok + i * kFinThreads + tid;
+        if (t < t1) add[i] += ex2_approx(sc[(size_t)(g0 + gi) * sp.pitch + t] - ls);
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kAccTok / kFinThreads; ++i) {
+    const int t = blk * kAccTok + i * kFinThreads + tid;
+    if (t < t1) w[t] += add[i];
   }
 }
 
@@ -741,6 +854,8 @@ Plan make_plan(int n_seq, int max_tokens, int heads, int kv_heads, int head_dim,
     sp.lse = take((size_t)n_seq * heads);
     sp.scores = take((size_t)n_seq * heads * max_tokens);
   }
+  sp.pitch = max_tokens;
+  sp.joins = n_seq * heads;
   return p;
 }
 
@@ -791,15 +906,11 @@ int launch_paged_attention(const DecodeArgs& a, int dtype, void* workspace, cuda
     if ((rc = record_cuda(e))) return rc;
   }
   ProfScope ps(SFM_PROF_ATTN_MERGE, s);
-  const unsigned joins = (unsigned)(a.c.n_seq * a.heads);
-  if (dtype == SFM_DTYPE_BF16)
-    rc = record_cuda(launch_dependent(paged_join_kernel<__nv_bfloat16>, joins, 128, 0, s, a, sp));
-  else
-    rc = record_cuda(launch_dependent(paged_join_kernel<float>, joins, 128, 0, s, a, sp));
-  if (rc || !a.weights) return rc;
   const int per_item = (a.c.max_tokens + kAccTok - 1) / kAccTok;
-  return record_cuda(launch_dependent(paged_weights_kernel, (unsigned)(a.c.n_seq * a.c.kv_heads * per_item),
-                                      kAccThreads, 0, s, a, sp, per_item));
+  const unsigned fin = (unsigned)(sp.joins + (a.weights ? a.c.n_seq * a.c.kv_heads * per_item : 0));
+  if (dtype == SFM_DTYPE_BF16)
+    return record_cuda(launch_dependent(paged_finish_kernel<__nv_bfloat16>, fin, kFinThreads, 0, s, a, sp, per_item));
+  return record_cuda(launch_dependent(paged_finish_kernel<float>, fin, kFinThreads, 0, s, a, sp, per_item));
 }
 
 }  // namespace sfm
