@@ -200,11 +200,12 @@ int sfm_attention_masked(const void* q, const void* k, const void* v, void* o, i
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(key_lo, 4) ||
       !aligned(key_hi, 4) || !aligned(slopes, 4))
     return SFM_EINVAL;
-  if (n_q > INT_MAX - 256 || n_kv > INT_MAX - 256 || !fits_grid((long long)n_q * n_heads)) return SFM_EUNSUPPORTED;
+  if (n_q > INT_MAX - 256 || n_kv > INT_MAX - 256 || !fits_grid((long long)n_q * n_heads) ||
+      !fits_grid(((long long)n_q / 32 + 1) * n_heads * 16)) return SFM_EUNSUPPORTED;
   const size_t need = masked_workspace(n_q, n_kv, n_heads, n_kv_heads, head_dim, dtype);
   if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 16)))) return SFM_EINVAL;
   MaskedArgs a{q, k, v, o, n_q, n_kv, n_heads, n_kv_heads, head_dim, key_lo, key_hi, softcap, slopes};
-  if (dtype == SFM_DTYPE_FP32) return launch_attention_masked_f32(a, (cudaStream_t)stream);
+  if (dtype == SFM_DTYPE_FP32) return launch_attention_masked_f32(a, workspace, (cudaStream_t)stream);
   CUtensorMap mq, mk, mv;
   rc = make_rows_map(&mq, q, n_q, n_heads, 128);
   if (!rc) rc = make_rows_map(&mk, k, n_kv, n_kv_heads, 128);

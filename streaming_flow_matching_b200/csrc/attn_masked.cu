@@ -33,6 +33,7 @@
 #include <math.h>
 
 #include "attn_masked.cuh"
+#include "dependent.cuh"
 #include "sm100.cuh"
 
 namespace sfm {
@@ -248,6 +249,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
+  // only CTA-local set-up so far: the kernel before (which may have made the ranges, q, k, v) is
+  // waited for here
+  grid_dependency_wait();
   // the Q tiles do not wait for the ranges (the barrier's own initialising thread loads them)
   const bool loads = !(args.fault & SFM_FAULT_ATTN_NO_LOADS);
   if (threadIdx.x == 0) {
@@ -750,37 +754,55 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Joins the splits of a (row, head): one warp each, 4 dims per lane.  A row no split of
-// which saw a key gets zeros.
+// Joins the splits of a (row, head): one warp each, 4 dims per lane (lanes past the head's
+// dims idle).  A row no split of which saw a key gets zeros.
+template <typename T>
 __global__ void __launch_bounds__(256)
     masked_join_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_part,
-                       __nv_bfloat16* __restrict__ o, long long rows_heads, int n_splits) {
+                       T* __restrict__ o, long long rows_heads, int dim, int n_splits) {
+  grid_dependency_wait();
   const long long gw = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (gw >= rows_heads) return;
-  float mx = -INFINITY;
-  for (int s = 0; s < n_splits; ++s) mx = fmaxf(mx, lse_part[s * rows_heads + gw]);
+  // lane s holds split s's log-sum-exp (at most 16 splits)
+  const float mine = lane < n_splits ? lse_part[lane * rows_heads + gw] : -INFINITY;
+  float mx = mine;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+  const bool bad = __any_sync(0xffffffffu, mine != mine);      // some split's sum was not a number
+  const float mine_w = mine == -INFINITY ? 0.f : exp2f(mine - mx);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  bool bad = false;                                            // some split's sum was not a number
 #pragma unroll 4
   for (int s = 0; s < n_splits; ++s) {
-    const float ls = lse_part[s * rows_heads + gw];
-    bad |= ls != ls;
-    if (ls == -INFINITY) continue;                             // the split saw no key of this row
-    const float4 p = reinterpret_cast<const float4*>(o_part + (s * rows_heads + gw) * D)[lane];
-    const float w = exp2f(ls - mx);
+    const float w = __shfl_sync(0xffffffffu, mine_w, s);
+    const bool none = __shfl_sync(0xffffffffu, mine == -INFINITY ? 1 : 0, s);
+    if (none || lane * 4 >= dim) continue;                     // the split saw no key of this row
+    const float4 p = reinterpret_cast<const float4*>(o_part + (s * rows_heads + gw) * dim)[lane];
     sum += w;
     acc.x = fmaf(w, p.x, acc.x);
     acc.y = fmaf(w, p.y, acc.y);
     acc.z = fmaf(w, p.z, acc.z);
     acc.w = fmaf(w, p.w, acc.w);
   }
+  if (lane * 4 >= dim) return;
   const float inv = bad ? NAN : sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-  uint2 b;
-  b.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-  b.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(o + gw * D)[lane] = b;
+  acc.x *= inv;
+  acc.y *= inv;
+  acc.z *= inv;
+  acc.w *= inv;
+  if constexpr (sizeof(T) == 2)
+    reinterpret_cast<uint2*>(o + gw * dim)[lane] = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+  else
+    reinterpret_cast<float4*>(o + gw * dim)[lane] = acc;
+}
+
+template <typename T>
+int launch_join(const float* o_part, const float* lse_part, void* o, long long rows_heads, int dim, int n_splits,
+                cudaStream_t s) {
+  ProfScope ps(SFM_PROF_ATTN_MERGE, s);
+  return record_cuda(launch_dependent(masked_join_kernel<T>, (unsigned)((rows_heads * 32 + 255) / 256), 256, 0, s,
+                                      o_part, lse_part, (T*)o, rows_heads, dim, n_splits));
 }
 
 // ------------------------------------------------------------------ fp32, CUDA cores
@@ -797,9 +819,13 @@ constexpr int f32_smem() {
 // (keys tx + 16 k) and 4 rows x 2 DV outputs.  Masked scores are skipped by weight 0 and
 // masked V rows by staging zeros for keys that no row of the tile sees; a key that only
 // some rows see and that holds a non-finite value is left out row by row.
+// n_splits > 1: the tiles of the rows' union are cut into that many runs, each writing a
+// normalised partial and its log-sum-exp.
 template <int DV>
 __global__ void __launch_bounds__(FTHREADS)
-    attn_masked_f32_kernel(const __grid_constant__ MaskedArgs a) {
+    attn_masked_f32_kernel(const __grid_constant__ MaskedArgs a, int n_splits, float* __restrict__ o_part,
+                           float* __restrict__ lse_part) {
+  grid_dependency_wait();
   constexpr int DD = 32 * DV, P = DD + 4, SP = FN + 4;
   extern __shared__ __align__(16) float fsm[];
   float* qs = fsm;
@@ -809,8 +835,9 @@ __global__ void __launch_bounds__(FTHREADS)
   __shared__ int red[2][FTHREADS / 32];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int h = blockIdx.x % a.heads;
+  const int split = blockIdx.x / a.heads % n_splits;
   const int qblocks = (a.n_q + FM - 1) / FM;
-  const int qb = qblocks - 1 - blockIdx.x / a.heads;
+  const int qb = qblocks - 1 - blockIdx.x / a.heads / n_splits;
   const int row0 = qb * FM;
   const int hk = h / (a.heads / a.kv_heads);
   const size_t ldq = (size_t)a.heads * DD, ldk = (size_t)a.kv_heads * DD;
@@ -860,7 +887,10 @@ __global__ void __launch_bounds__(FTHREADS)
 #pragma unroll
     for (int e = 0; e < 2 * DV; ++e) o[i][e] = 0.f;
   }
-  for (int k0 = u_lo < u_hi ? u_lo / FN * FN : 0; k0 < u_hi; k0 += FN) {
+  const int tile0 = u_lo < u_hi ? u_lo / FN : 0, tiles = u_lo < u_hi ? (u_hi + FN - 1) / FN - tile0 : 0;
+  const int run = (tiles + n_splits - 1) / n_splits;
+  const int k_end = (tile0 + min(tiles, (split + 1) * run)) * FN;
+  for (int k0 = (tile0 + min(tiles, split * run)) * FN; k0 < k_end; k0 += FN) {
     __syncthreads();
     bool odd = false;                                          // a non-finite V element here
     for (int x = tid; x < FN * (DD / 4); x += FTHREADS) {
@@ -964,7 +994,7 @@ __global__ void __launch_bounds__(FTHREADS)
         }
     }
   }
-  float* out = reinterpret_cast<float*>(a.o) + (size_t)h * DD;
+  float* out = (n_splits > 1 ? o_part + (size_t)split * a.n_q * ldq : reinterpret_cast<float*>(a.o)) + (size_t)h * DD;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = row0 + ty * 4 + i;
@@ -974,43 +1004,44 @@ __global__ void __launch_bounds__(FTHREADS)
     for (int e = 0; e < DV; ++e)
       *reinterpret_cast<float2*>(out + (size_t)row * ldq + 2 * tx + 32 * e) =
           have ? make_float2(o[i][2 * e] / l[i], o[i][2 * e + 1] / l[i]) : make_float2(0.f, 0.f);
+    if (n_splits > 1 && tx == 0)
+      lse_part[((size_t)split * a.n_q + row) * a.heads + h] = have ? m[i] + log2f(l[i]) : -INFINITY;
   }
 }
 
 template <int DV>
-int run_f32(const MaskedArgs& a, cudaStream_t s) {
+cudaError_t run_f32(const MaskedArgs& a, int n_splits, float* o_part, float* lse_part, cudaStream_t s) {
   constexpr int smem = f32_smem<DV>();
   const cudaError_t e =
       cudaFuncSetAttribute(attn_masked_f32_kernel<DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return record_cuda(e);
-  const unsigned grid = (unsigned)((a.n_q + FM - 1) / FM) * (unsigned)a.heads;
-  attn_masked_f32_kernel<DV><<<grid, FTHREADS, smem, s>>>(a);
-  return record_cuda(cudaGetLastError());
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)((a.n_q + FM - 1) / FM) * (unsigned)a.heads * (unsigned)n_splits;
+  return launch_dependent(attn_masked_f32_kernel<DV>, grid, FTHREADS, smem, s, a, n_splits, o_part, lse_part);
 }
 
 bool pairs_heads(int heads, int kv_heads) { return (heads / kv_heads) % 2 == 0; }
 
-int base_ctas(int n_q, int heads, int kv_heads) {
+long long base_ctas(int n_q, int heads, int kv_heads) {
   const bool p = pairs_heads(heads, kv_heads);
   const int rows = p ? BQ : 2 * BQ;
-  return (n_q + rows - 1) / rows * (p ? heads / 2 : heads);
+  return (long long)((n_q + rows - 1) / rows) * (p ? heads / 2 : heads);
 }
 
 }  // namespace
 
-// Splits fill the SMs when the query blocks alone do not; each keeps at least two key
-// tiles of the longest possible range.
-int masked_splits(int n_q, int n_kv, int heads, int kv_heads) {
-  const int ctas = base_ctas(n_q, heads, kv_heads);
-  const int tiles = (n_kv + BKV - 1) / BKV;
-  int s = kSms / ctas;
-  if (s > tiles / 2) s = tiles / 2;
+// Splits fill the SMs when the query blocks alone do not.  bf16: one CTA per SM, each at
+// least two key tiles of the longest possible range; fp32: four per SM, each at least four.
+int masked_splits(int n_q, int n_kv, int heads, int kv_heads, int dtype) {
+  const bool tc = dtype == SFM_DTYPE_BF16;
+  const long long ctas = tc ? base_ctas(n_q, heads, kv_heads) : (long long)((n_q + FM - 1) / FM) * heads;
+  const int tiles = tc ? (n_kv + BKV - 1) / BKV / 2 : (n_kv + FN - 1) / FN / 4;
+  const long long want = (tc ? kSms : 4 * kSms) / ctas;
+  const int s = want < tiles ? (int)want : tiles;
   return s < 1 ? 1 : s > kMaxKeySplits ? kMaxKeySplits : s;
 }
 
 size_t masked_workspace(int n_q, int n_kv, int heads, int kv_heads, int head_dim, int dtype) {
-  if (dtype != SFM_DTYPE_BF16) return 0;
-  const int sp = masked_splits(n_q, n_kv, heads, kv_heads);
+  const int sp = masked_splits(n_q, n_kv, heads, kv_heads, dtype);
   if (sp == 1) return 0;
   const size_t b = (size_t)sp * n_q * heads * (head_dim + 1) * sizeof(float);
   return (b + 15) / 16 * 16;
@@ -1024,7 +1055,7 @@ int launch_attention_masked_tc(const MaskedArgs& a, const CUtensorMap& mq, const
   t.hgroups = t.paired ? a.heads / 2 : a.heads;
   const int rows = t.paired ? BQ : 2 * BQ;
   t.qblocks = (a.n_q + rows - 1) / rows;
-  t.n_splits = masked_splits(a.n_q, a.n_kv, a.heads, a.kv_heads);
+  t.n_splits = masked_splits(a.n_q, a.n_kv, a.heads, a.kv_heads, SFM_DTYPE_BF16);
   const long long rows_heads = (long long)a.n_q * a.heads;
   if (t.n_splits > 1) {
     t.o_part = (float*)workspace;
@@ -1041,24 +1072,35 @@ int launch_attention_masked_tc(const MaskedArgs& a, const CUtensorMap& mq, const
   int rc;
   {
     ProfScope ps(SFM_PROF_ATTN, s);
-    kernel<<<(unsigned)(t.qblocks * t.hgroups * t.n_splits), THREADS, SMEM, s>>>(mq, mk, mv, t);
-    rc = record_cuda(cudaGetLastError());
+    rc = record_cuda(launch_dependent(kernel, (unsigned)(t.qblocks * t.hgroups * t.n_splits), THREADS, SMEM, s, mq, mk,
+                                      mv, t));
   }
   if (rc || t.n_splits == 1) return rc;
-  ProfScope ps(SFM_PROF_ATTN_MERGE, s);
-  masked_join_kernel<<<(unsigned)((rows_heads * 32 + 255) / 256), 256, 0, s>>>(
-      t.o_part, t.lse_part, (__nv_bfloat16*)a.o, rows_heads, t.n_splits);
-  return record_cuda(cudaGetLastError());
+  return launch_join<__nv_bfloat16>(t.o_part, t.lse_part, a.o, rows_heads, D, t.n_splits, s);
 }
 
-int launch_attention_masked_f32(const MaskedArgs& a, cudaStream_t s) {
-  ProfScope ps(SFM_PROF_ATTN, s);
-  switch (a.head_dim / 32) {
-    case 1: return run_f32<1>(a, s);
-    case 2: return run_f32<2>(a, s);
-    case 3: return run_f32<3>(a, s);
-    default: return run_f32<4>(a, s);
+int launch_attention_masked_f32(const MaskedArgs& a, void* workspace, cudaStream_t s) {
+  const int n_splits = masked_splits(a.n_q, a.n_kv, a.heads, a.kv_heads, SFM_DTYPE_FP32);
+  const long long rows_heads = (long long)a.n_q * a.heads;
+  float *o_part = nullptr, *lse_part = nullptr;
+  if (n_splits > 1) {
+    o_part = (float*)workspace;
+    lse_part = o_part + (size_t)n_splits * rows_heads * a.head_dim;
   }
+  int rc;
+  {
+    ProfScope ps(SFM_PROF_ATTN, s);
+    cudaError_t e;
+    switch (a.head_dim / 32) {
+      case 1: e = run_f32<1>(a, n_splits, o_part, lse_part, s); break;
+      case 2: e = run_f32<2>(a, n_splits, o_part, lse_part, s); break;
+      case 3: e = run_f32<3>(a, n_splits, o_part, lse_part, s); break;
+      default: e = run_f32<4>(a, n_splits, o_part, lse_part, s); break;
+    }
+    rc = record_cuda(e);
+  }
+  if (rc || n_splits == 1) return rc;
+  return launch_join<float>(o_part, lse_part, a.o, rows_heads, a.head_dim, n_splits, s);
 }
 
 int launch_attention_bounds(const BoundsArgs& a, cudaStream_t s) {

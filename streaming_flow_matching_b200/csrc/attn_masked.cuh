@@ -20,12 +20,12 @@ struct MaskedArgs {
   const float* slopes;    // [H], null: no bias
 };
 
-// bf16 key splits of a call (a function of the shape alone) and the scratch they need.
-int masked_splits(int n_q, int n_kv, int heads, int kv_heads);
+// Key splits of a call (a function of the shape alone) and the scratch they need.
+int masked_splits(int n_q, int n_kv, int heads, int kv_heads, int dtype);
 size_t masked_workspace(int n_q, int n_kv, int heads, int kv_heads, int head_dim, int dtype);
 int launch_attention_masked_tc(const MaskedArgs& a, const CUtensorMap& mq, const CUtensorMap& mk,
                                const CUtensorMap& mv, void* workspace, const Guard& gd, cudaStream_t s);
-int launch_attention_masked_f32(const MaskedArgs& a, cudaStream_t s);
+int launch_attention_masked_f32(const MaskedArgs& a, void* workspace, cudaStream_t s);
 
 struct BoundsArgs {
   int n_q, n_kv;

@@ -159,11 +159,13 @@ def test_arbitrary_ranges(cuda_device, dtype, d):
     run(q, k, v, ints([5] * n_q), ints([5] * n_q))          # every range empty
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 32), (F32, 96), (F32, 128)])
 @pytest.mark.parametrize("n_q,n_kv,h,hk", [(1, 20000, 2, 1), (3, 5000, 1, 1), (130, 9000, 4, 1)])
-def test_key_splits_join(cuda_device, n_q, n_kv, h, hk):
+def test_key_splits_join(cuda_device, dtype, d, n_q, n_kv, h, hk):
     # few rows over many keys run in splits: rows that see no key of a split, or of any
-    assert L.lib.sfm_attention_masked_workspace_bytes(n_q, n_kv, h, hk, 128, L.SFM_DTYPE_BF16) > 0
-    q, k, v = make(n_q, n_kv, h, hk, 128, BF, seed=n_kv)
+    code = L.SFM_DTYPE_BF16 if dtype == BF else L.SFM_DTYPE_FP32
+    assert L.lib.sfm_attention_masked_workspace_bytes(n_q, n_kv, h, hk, d, code) > 0
+    q, k, v = make(n_q, n_kv, h, hk, d, dtype, seed=n_kv)
     run(q, k, v, softcap=30.0)
     hi = ints([0 if i % 3 == 2 else 100 + i for i in range(n_q)])
     out = run(q, k, v, None, hi)
