@@ -716,7 +716,7 @@ __device__ void join_ml(const Split& sp, int G, int h, const Parts& p, int lane,
   *l = sum;
 }
 
-constexpr int kFinThreads = 256, kFinWarps = kFinThreads / 32, kAccTok = 1024;
+constexpr int kFinThreads = 256, kFinWarps = kFinThreads / 32, kAccTok = 2048;
 
 // The finishing kernel.  Its first CTAs join, one per (sequence, query head): a sequence
 // finished by one CTA is left alone, an empty one gets zeros; the partials are summed in a

@@ -90,12 +90,13 @@ __global__ void __launch_bounds__(kAppendThreads)
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kBatch = 8;       // loads in flight per thread
 constexpr int kHeldRanks = 48 * 1024;   // ranks in shared memory: 192 KB
 
 // Rank of a token as an unsigned number, larger = kept first: NaN below every number,
 // -0 equal to +0, protected tokens above all.
-__device__ __forceinline__ unsigned rank_of(float w, int pos, int first, long long recent_from) {
-  if (pos < first || pos >= recent_from) return 0xFFFFFFFFu;
+__device__ __forceinline__ unsigned rank_of(float w, int pos, int first, bool recent, int recent_from) {
+  if (pos < first || (recent && pos >= recent_from)) return 0xFFFFFFFFu;
   if (w != w) return 0u;
   const unsigned b = __float_as_uint(w + 0.f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
@@ -109,44 +110,45 @@ __device__ __forceinline__ int warp_sum(int v) {
 
 // lists: per (sequence, key head) `room` evicted slots then `room` moved slots; counts: one each.
 // The ranks are made once and kept in shared memory (`held` of them at most; a longer
-// sequence makes them again in each of the five passes): 36,000 slots took 90 us when every
-// pass read weights and positions from L2.
-__global__ void __launch_bounds__(kSelThreads)
-    evict_select_kernel(const __grid_constant__ EvictArgs a, int* __restrict__ counts,
-                        int* __restrict__ lists, int room, int held) {
+// sequence makes them again in each of its five passes).  Bound by instructions: one CTA
+// handles one sequence and key head, so the passes over shared memory are kept short.
+struct SelectShared {
+  unsigned hist[kBins];
+  int part[3][kSelWarps];
+  unsigned digit;
+  int above;
+};
+
+template <bool HOLD>
+__device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict__ counts, int* __restrict__ lists,
+                                             int room, int n, SelectShared& sh) {
   extern __shared__ unsigned ranks[];
-  __shared__ unsigned hist[kBins];
-  __shared__ int part[3][kSelWarps];
-  __shared__ unsigned sh_digit;
-  __shared__ int sh_above;
-  const int item = blockIdx.x, seq = item / a.c.kv_heads;
+  auto& hist = sh.hist;
+  auto& part = sh.part;
+  const int item = blockIdx.x, keep = a.keep;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n = cache_len(a.c, seq, a.err), keep = a.keep;
-  if (n <= keep) {
-    if (tid == 0) counts[item] = 0;
-    return;
-  }
   const float* w = a.weights + (size_t)item * a.cap;
   const int* pos = a.positions + (size_t)item * a.cap;
   // newest position
   int mx = INT_MIN;
-#pragma unroll 8
-  for (int t = tid; t < n; t += kSelThreads) mx = max(mx, __ldg(pos + t));
+  for (int t0 = tid; t0 < n; t0 += kBatch * kSelThreads) {
+    int p[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) p[u] = t0 + u * kSelThreads < n ? __ldg(pos + t0 + u * kSelThreads) : INT_MIN;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) mx = max(mx, p[u]);
+  }
   mx = __reduce_max_sync(0xffffffffu, mx);
   if (lane == 0) part[0][warp] = mx;
   __syncthreads();
   mx = __reduce_max_sync(0xffffffffu, part[0][lane]);
   __syncthreads();
-  const long long recent_from = (long long)mx - a.n_recent + 1;
-  const bool hold = n <= held;
-  auto make_rank = [&](int t) { return rank_of(__ldg(w + t), __ldg(pos + t), a.n_first, recent_from); };
-  if (hold) {
-#pragma unroll 8
-    for (int t = tid; t < n; t += kSelThreads) ranks[t] = make_rank(t);
-  }
-  auto rank = [&](int t) { return hold ? ranks[t] : make_rank(t); };
+  const int recent_from = (int)max((long long)INT_MIN, (long long)mx - a.n_recent + 1);   // (n_recent > 0)
+  auto make_rank = [&](int t) { return rank_of(__ldg(w + t), __ldg(pos + t), a.n_first, a.n_recent > 0, recent_from); };
+  auto rank = [&](int t) { return HOLD ? ranks[t] : make_rank(t); };
   // the keep-th largest rank, digit by digit: `want` of the ranks that match the
-  // prefix found so far are still to be taken
+  // prefix found so far are still to be taken.  The first digit is counted as the
+  // ranks are made.
   unsigned prefix = 0, mask = 0;
   int want = keep;
   for (int d = 0; d < 3; ++d) {
@@ -154,10 +156,30 @@ __global__ void __launch_bounds__(kSelThreads)
     const unsigned bins = d == 2 ? 1024u : 2048u;
     for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int t = tid; t < n; t += kSelThreads) {
-      const unsigned r = rank(t);
-      if ((r & mask) == prefix) atomicAdd(&hist[(r >> shift) & (bins - 1)], 1u);
+    if (d == 0) {
+      for (int t0 = tid; t0 < n; t0 += kBatch * kSelThreads) {
+        float wv[kBatch];
+        int pv[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int t = min(t0 + u * kSelThreads, n - 1);      // (a slot past the end: not used below)
+          wv[u] = __ldg(w + t);
+          pv[u] = __ldg(pos + t);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int t = t0 + u * kSelThreads;
+          const unsigned r = rank_of(wv[u], pv[u], a.n_first, a.n_recent > 0, recent_from);
+          if (HOLD && t < n) ranks[t] = r;
+          if (t < n) atomicAdd(&hist[r >> 21], 1u);
+        }
+      }
+    } else {
+#pragma unroll 8
+      for (int t = tid; t < n; t += kSelThreads) {
+        const unsigned r = rank(t);
+        if ((r & mask) == prefix) atomicAdd(&hist[(r >> shift) & (bins - 1)], 1u);
+      }
     }
     __syncthreads();
     // bins from the top: thread i holds bins (2047 - 2 i), (2046 - 2 i)
@@ -170,71 +192,103 @@ __global__ void __launch_bounds__(kSelThreads)
     }
     if (lane == 31) part[0][warp] = inc;
     __syncthreads();
-    int before = 0;
-    for (int k = 0; k < warp; ++k) before += part[0][k];
+    const int before = warp_sum(lane < warp ? part[0][lane] : 0);
     const int exc = before + inc - c0 - c1;
     if (exc < want && want <= exc + c0) {
-      sh_digit = kBins - 1 - 2 * tid;
-      sh_above = exc;
+      sh.digit = kBins - 1 - 2 * tid;
+      sh.above = exc;
     } else if (exc + c0 < want && want <= exc + c0 + c1) {
-      sh_digit = kBins - 2 - 2 * tid;
-      sh_above = exc + c0;
+      sh.digit = kBins - 2 - 2 * tid;
+      sh.above = exc + c0;
     }
     __syncthreads();
-    prefix |= sh_digit << shift;
+    prefix |= sh.digit << shift;
     mask |= (bins - 1) << shift;
-    want -= sh_above;
+    want -= sh.above;
     __syncthreads();
   }
-  // ranks above `prefix` stay, and of those equal to it the first `want` by slot.
-  // Each warp walks a contiguous run of slots: its number of ties first, then the lists.
+  // Ranks above `prefix` stay, and of those equal to it the first `want` by slot.  Each warp
+  // walks a contiguous run of slots, first counting: what it will list follows from the
+  // ties before it.
   const int per = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
   const int t0 = min(n, warp * per), t1 = min(n, t0 + per);
-  int ties = 0;
+  const int mid = min(max(keep, t0), t1);                      // the run's slots < keep end here
+  int tie_lo = 0, tie_hi = 0, n_out = 0, n_mv = 0;
 #pragma unroll 4
-  for (int t = t0 + lane; t < t1; t += 32) ties += rank(t) == prefix;
-  ties = warp_sum(ties);
-  if (lane == 0) part[0][warp] = ties;
+  for (int t = t0 + lane; t < mid; t += 32) {
+    const unsigned r = rank(t);
+    tie_lo += r == prefix;
+    n_out += r < prefix;
+  }
+#pragma unroll 4
+  for (int t = mid + lane; t < t1; t += 32) {
+    const unsigned r = rank(t);
+    tie_hi += r == prefix;
+    n_mv += r > prefix;
+  }
+  tie_lo = warp_sum(tie_lo);
+  tie_hi = warp_sum(tie_hi);
+  n_out = warp_sum(n_out);
+  n_mv = warp_sum(n_mv);
+  if (lane == 0) part[0][warp] = tie_lo + tie_hi;
   __syncthreads();
-  int tie_base = 0;
-  for (int k = 0; k < warp; ++k) tie_base += part[0][k];
-  int n_out = 0, n_mv = 0, out_base = 0, mv_base = 0;
+  const int tie_base = warp_sum(lane < warp ? part[0][lane] : 0);
+  const int left = max(0, want - tie_base);                    // ties of this run that stay
+  n_out += max(0, tie_lo - left);
+  n_mv += min(tie_hi, max(0, left - tie_lo));
+  if (lane == 0) {
+    part[1][warp] = n_out;
+    part[2][warp] = n_mv;
+  }
+  __syncthreads();
+  int no = warp_sum(lane < warp ? part[1][lane] : 0), nm = warp_sum(lane < warp ? part[2][lane] : 0);
   int* outs = lists + (size_t)item * 2 * room;
   int* mvs = outs + room;
-  for (int pass = 0; pass < 2; ++pass) {
-    int tie = tie_base, no = out_base, nm = mv_base;
-    for (int t = t0; t < t1; t += 32) {
-      const int x = t + lane;
-      const unsigned r = x < t1 ? rank(x) : 0u;
-      const bool eq = x < t1 && r == prefix;
-      const unsigned eqs = __ballot_sync(0xffffffffu, eq);
-      const unsigned lower = (1u << lane) - 1u;
-      const bool stay = x < t1 && (r > prefix || (eq && tie + __popc(eqs & lower) < want));
-      const unsigned out_m = __ballot_sync(0xffffffffu, x < t1 && x < keep && !stay);
-      const unsigned mv_m = __ballot_sync(0xffffffffu, x >= keep && stay);
-      if (pass) {
-        if ((out_m >> lane) & 1u) outs[no + __popc(out_m & lower)] = x;
-        if ((mv_m >> lane) & 1u) mvs[nm + __popc(mv_m & lower)] = x;
+  const unsigned lower = (1u << lane) - 1u;
+  int tie = tie_base;
+  auto walk = [&](int from, int to, bool behind, int* list, int at) {
+    for (int t = from; t < to; t += 32 * kBatch) {
+      unsigned rv[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int x = t + 32 * u + lane;
+        rv[u] = x < to ? rank(x) : 0u;
       }
-      tie += __popc(eqs);
-      no += __popc(out_m);
-      nm += __popc(mv_m);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int x = t + 32 * u + lane;
+        bool stay = rv[u] > prefix;
+        if (tie_lo + tie_hi > 0) {                             // warp-uniform: most runs have none
+          const bool eq = x < to && rv[u] == prefix;
+          const unsigned eqs = __ballot_sync(0xffffffffu, eq);
+          stay = stay || (eq && tie + __popc(eqs & lower) < want);
+          tie += __popc(eqs);
+        }
+        const bool take = x < to && stay == behind;
+        const unsigned m = __ballot_sync(0xffffffffu, take);
+        if (take) list[at + __popc(m & lower)] = x;
+        at += __popc(m);
+      }
     }
-    if (pass == 0) {
-      n_out = no;
-      n_mv = nm;
-      if (lane == 0) {
-        part[1][warp] = n_out;
-        part[2][warp] = n_mv;
-      }
-      __syncthreads();
-      for (int k = 0; k < warp; ++k) {
-        out_base += part[1][k];
-        mv_base += part[2][k];
-      }
-    } else if (tid == kSelThreads - 1) {
-      counts[item] = nm;               // = no: both are keep minus the kept slots < keep
-    }
+    return at;
+  };
+  walk(t0, mid, false, outs, no);
+  nm = walk(mid, t1, true, mvs, nm);
+  // as many slots were evicted before `keep` as are kept behind it
+  if (warp == kSelWarps - 1 && lane == 0) counts[item] = nm;
+}
+
+__global__ void __launch_bounds__(kSelThreads)
+    evict_select_kernel(const __grid_constant__ EvictArgs a, int* __restrict__ counts,
+                        int* __restrict__ lists, int room, int held) {
+  __shared__ SelectShared sh;
+  const int n = cache_len(a.c, blockIdx.x / a.c.kv_heads, a.err);
+  if (n <= a.keep) {
+    if (threadIdx.x == 0) counts[blockIdx.x] = 0;
+  } else if (n <= held) {
+    evict_select<true>(a, counts, lists, room, n, sh);
+  } else {
+    evict_select<false>(a, counts, lists, room, n, sh);
   }
 }
 
