@@ -420,6 +420,7 @@ SFM_API int sfm_fm_solve_exact_velocity(const sfm_handle* h, const float* z0, fl
  *     (infinities and NaN included).
  *   - bf16 (D_h = 128): P is rounded to bf16 for the product with V, sums and
  *     statistics are fp32.  fp32 (D_h a multiple of 32, <= 128): fp32 throughout.
+ *   - o is a buffer other than q, k, v (SFM_EINVAL if o == q).
  *   - slopes need n_kv >= n_q (the queries sit at the last n_q keys' positions).
  *   - workspace: sfm_attention_masked_workspace_bytes(...) bytes, 16-byte aligned
  *     (may be NULL when that is 0); nothing in it has to be set, and calls that
@@ -496,7 +497,7 @@ SFM_API int sfm_paged_append(const void* k, const void* v, void* k_pages, void* 
  *   o = sum_t softmax(s)_t v_t over slots t < lengths[s]   (length 0: zeros)
  *   weights[s][h_kv][t] += sum of softmax(s)_t over the query heads of h_kv
  * lengths counts the slots to attend to (the new token's own, once appended,
- * included).  positions and q_positions go together and need slopes.  Any number of
+ * included).  o is a buffer other than q (SFM_EINVAL).  positions and q_positions go together and need slopes.  Any number of
  * query heads per key head.  Results do not depend on timing (partials are joined
  * in a fixed order).  workspace: the size for max_tokens = max_pages * page_size,
  * or cap where that is smaller and the call has state arrays.

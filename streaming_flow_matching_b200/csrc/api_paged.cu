@@ -103,7 +103,7 @@ int sfm_paged_attention(const void* q, const void* k_pages, const void* v_pages,
                         size_t workspace_bytes, void* stream) {
   int rc = check_heads(n_heads, n_kv_heads, head_dim, dtype);
   if (rc) return rc;
-  if (!q || !o || !aligned(q, 16) || !aligned(o, 16)) return SFM_EINVAL;
+  if (!q || !o || o == q || !aligned(q, 16) || !aligned(o, 16)) return SFM_EINVAL;
   if (!(softcap >= 0.f) || isinf(softcap)) return SFM_EINVAL;
   const bool state = positions || weights;
   if ((state && cap < 1) || ((positions != nullptr) != (q_positions != nullptr)) || (positions && !slopes))
@@ -194,7 +194,7 @@ int sfm_attention_masked(const void* q, const void* k, const void* v, void* o, i
                          void* stream) {
   int rc = check_heads(n_heads, n_kv_heads, head_dim, dtype);
   if (rc) return rc;
-  if (!q || !k || !v || !o || n_q < 1 || n_kv < 1) return SFM_EINVAL;
+  if (!q || !k || !v || !o || o == q || n_q < 1 || n_kv < 1) return SFM_EINVAL;
   if (slopes && n_kv < n_q) return SFM_EINVAL;      // the bias needs the queries' positions among the keys
   if (!(softcap >= 0.f) || isinf(softcap)) return SFM_EINVAL;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(key_lo, 4) ||

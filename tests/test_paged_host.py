@@ -19,7 +19,7 @@ def append(**kw):
 
 
 def attention(**kw):
-    a = dict(q=P, kp=P, vp=P, table=P, lengths=P, o=P, n_seq=2, n_pages=8, page=16, width=4, h=4, hk=2, d=128,
+    a = dict(q=P, kp=P, vp=P, table=P, lengths=P, o=2 * P, n_seq=2, n_pages=8, page=16, width=4, h=4, hk=2, d=128,
              dtype=BF, cap=0.0, slopes=P, positions=P, q_positions=P, weights=P, room=64, ws=P, ws_bytes=1 << 40)
     a.update(kw)
     return L.lib.sfm_paged_attention(*a.values(), None)
@@ -33,7 +33,7 @@ def evict(**kw):
 
 
 def masked(**kw):
-    a = dict(q=P, k=P, v=P, o=P, n_q=4, n_kv=8, h=4, hk=2, d=128, dtype=BF, lo=P, hi=P, cap=0.0, slopes=P, ws=P,
+    a = dict(q=P, k=P, v=P, o=2 * P, n_q=4, n_kv=8, h=4, hk=2, d=128, dtype=BF, lo=P, hi=P, cap=0.0, slopes=P, ws=P,
              ws_bytes=1 << 40)
     a.update(kw)
     return L.lib.sfm_attention_masked(*a.values(), None)
@@ -66,7 +66,8 @@ def test_append_arguments(bad):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(q=None), dict(o=None), dict(q=P + 8), dict(o=P + 2), dict(h=3), dict(h=0), dict(cap=-1.0), dict(cap=INF),
+    dict(q=None), dict(o=None), dict(o=P), dict(q=P + 8), dict(o=P + 2), dict(h=3), dict(h=0), dict(cap=-1.0),
+    dict(cap=INF),
     dict(cap=NAN), dict(positions=None), dict(q_positions=None), dict(slopes=None), dict(room=0), dict(ws=None),
     dict(ws=P + 8), dict(ws_bytes=16), dict(slopes=P + 2)])
 def test_attention_arguments(bad):
@@ -82,7 +83,7 @@ def test_evict_arguments(bad):
 
 @pytest.mark.parametrize("bad,code", [
     (dict(q=None), L.SFM_EINVAL), (dict(k=None), L.SFM_EINVAL), (dict(v=None), L.SFM_EINVAL),
-    (dict(o=None), L.SFM_EINVAL), (dict(n_q=0), L.SFM_EINVAL), (dict(n_kv=0), L.SFM_EINVAL),
+    (dict(o=None), L.SFM_EINVAL), (dict(o=P), L.SFM_EINVAL), (dict(n_q=0), L.SFM_EINVAL), (dict(n_kv=0), L.SFM_EINVAL),
     (dict(h=3), L.SFM_EINVAL), (dict(hk=0), L.SFM_EINVAL), (dict(dtype=3), L.SFM_EINVAL),
     (dict(d=64), L.SFM_EUNSUPPORTED), (dict(d=33, dtype=F32), L.SFM_EUNSUPPORTED),
     (dict(cap=-0.5), L.SFM_EINVAL), (dict(cap=NAN), L.SFM_EINVAL), (dict(cap=INF), L.SFM_EINVAL),
