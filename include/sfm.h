@@ -417,7 +417,8 @@ SFM_API int sfm_fm_solve_exact_velocity(const sfm_handle* h, const float* z0, fl
  * to it); slopes: device fp32 [n_heads] or NULL.
  *   - A query whose range is empty, or all of whose scores are -inf, gets zeros.
  *   - Keys outside a query's range do not reach it whatever K and V hold there
- *     (infinities and NaN included).
+ *     (infinities and NaN included).  An infinity of V inside the range gives that
+ *     infinity, or NaN where its weight is below 2^-126 (0 times infinity).
  *   - bf16 (D_h = 128): P is rounded to bf16 for the product with V, sums and
  *     statistics are fp32.  fp32 (D_h a multiple of 32, <= 128): fp32 throughout.
  *   - o is a buffer other than q, k, v (SFM_EINVAL if o == q).

@@ -16,7 +16,7 @@
 //               TMEM), alternating the tiles
 //   warps 4-11  softmax, thread = query row: a look at the largest product, then P against
 //               the running max, which moves only when a score passes it by 2^8
-//   warp 2      makes V safe: a masked key has weight 0, and 0 x inf or 0 x NaN would
+//   warps 2-3   make V safe: a masked key has weight 0, and 0 x inf or 0 x NaN would
 //               still reach rows that may not see it.  In key tiles that some row does not
 //               see whole it scans V and replaces non-finite elements by 0; if it found
 //               any, the rows that do see them get them added back at the end (a row's sum
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < VST; ++i) {
       mbar_init(&v_full[i], 1);
-      mbar_init(&v_ok[i], 1);
+      mbar_init(&v_ok[i], 2);
       mbar_init(&v_empty[i], 1);
     }
     for (int t = 0; t < QT; ++t) {
@@ -278,12 +278,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (i < m_.n_q) {                                          // rows past the end see all, write nothing
       live = true;
       row_range(m_, i, &my_lo, &my_hi);
-      if (my_hi > my_lo) {
-        u_lo = my_lo;
-        u_hi = my_hi;
+      if (my_hi > my_lo) {                                     // an empty row's products are not used
+        u_lo = n_lo = my_lo;
+        u_hi = n_hi = my_hi;
       }
-      n_lo = my_lo;
-      n_hi = my_hi;
     }
     u_lo = __reduce_min_sync(0xffffffffu, u_lo);
     u_hi = __reduce_max_sync(0xffffffffu, u_hi);
@@ -300,16 +298,25 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int all_lo = INT_MAX, all_hi = 0, full_lo = 0, full_hi = INT_MAX;
+  // key tiles that some row of each query tile sees, and keys that all its rows see
+  int see0[QT], see1[QT], full_lo[QT], full_hi[QT];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    all_lo = min(all_lo, red[w]);
-    all_hi = max(all_hi, red[8 + w]);
-    full_lo = max(full_lo, red[16 + w]);
-    full_hi = min(full_hi, red[24 + w]);
+  for (int t = 0; t < QT; ++t) {
+    int lo = INT_MAX, hi = 0;
+    full_lo[t] = 0;
+    full_hi[t] = INT_MAX;
+#pragma unroll
+    for (int w = 4 * t; w < 4 * t + 4; ++w) {
+      lo = min(lo, red[w]);
+      hi = max(hi, red[8 + w]);
+      full_lo[t] = max(full_lo[t], red[16 + w]);
+      full_hi[t] = min(full_hi[t], red[24 + w]);
+    }
+    see0[t] = lo < hi ? lo / BKV : INT_MAX;
+    see1[t] = lo < hi ? (hi + BKV - 1) / BKV : 0;
   }
-  const int u0 = all_lo < all_hi ? all_lo / BKV : 0;
-  const int u1 = all_lo < all_hi ? (all_hi + BKV - 1) / BKV : 0;
+  const int u1 = max(see1[0], see1[1]);
+  const int u0 = min(min(see0[0], see0[1]), u1);
   const int tps = (u1 - u0 + args.n_splits - 1) / args.n_splits;
   const int t0 = min(u1, u0 + split * tps);
   const int T = min(u1, t0 + tps) - t0;
@@ -322,10 +329,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     near = min(max(pos / BKV - t0, 0), T - 1);
   }
   auto tile_at = [&](int i) { return !BIAS ? t0 + i : t0 + (i <= near ? near - i : i); };
-  // a key tile (the j-th in order) inside every row's range
+  // some row of query tile t sees the key tile
+  auto sees = [&](int t, int k) { return k >= see0[t] && k < see1[t]; };
+  // a key tile (the j-th in order) that the query tiles which see anything of it see whole
   auto whole = [&](int j) {
-    const int k = tile_at(j) * BKV;
-    return k >= full_lo && k + BKV <= full_hi;
+    const int k = tile_at(j);
+    bool w = true;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) w = w && (!sees(t, k) || (k * BKV >= full_lo[t] && (k + 1) * BKV <= full_hi[t]));
+    return w;
   };
 
   if (warp == 0) {
@@ -376,7 +388,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr uint32_t idesc_s = idesc_bf16(BQ, BKV, false, false);
       constexpr uint32_t idesc_o = idesc_bf16(BQ, D, false, true);
       bool ok = mbar_wait(q_full, 0, abort, args.err, 0x403, args.wait_ns), issued = false;
-      auto issue_s = [&](int t, int ks) {
+      int gt[QT] = {0, 0};                                     // S products issued for each query tile
+      bool pv[QT] = {false, false};                            // the tile has had a P V
+      auto issue_s = [&](int t, int ks) -> bool {              // S_t = Q_t K^T from K stage ks
+        // S_t overwrites P_t: wait until its P V has completed
+        if (pv[t] && !mbar_wait(&o_done[t], (uint32_t)((gt[t] - 1) & 1), abort, args.err, 0x40B, args.wait_ns))
+          return false;
+        tc_fence_after();
         const uint32_t qa = base + OFF_Q + t * TILE, ka = base + OFF_K + ks * TILE;
         const uint32_t d = tmem + (uint32_t)(t * 256);
 #pragma unroll
@@ -387,18 +405,25 @@ __global__ void __launch_bounds__(THREADS, 1)
           umma_bf16(d, da, db, idesc_s, kk > 0 ? 1u : 0u);
         }
         umma_commit(&s_full[t]);
+        ++gt[t];
         issued = true;
+        return true;
       };
       if (ok && (ok = mbar_wait(&k_full[0], 0, abort, args.err, 0x404, args.wait_ns))) {
-        tc_fence_after();
-        issue_s(0, 0);
-        issue_s(1, 0);
+        const int k0 = tile_at(0);
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+          if (sees(t, k0)) issue_s(t, 0);
         umma_commit(&k_empty[0]);
       }
+      // per key tile j: P_A V, S_A(j+1), P_B V, S_B(j+1) -- tile A never waits on tile B, so
+      // the two softmax warpgroups run half a period apart; a query tile skips the key tiles
+      // that it sees nothing of
       for (int j = 0; j < T && ok; ++j) {
         const int vs = j % VST;
         const bool more = j + 1 < T;
         const int ks = (j + 1) % KST;
+        const int k0 = tile_at(j), k1 = tile_at(j + 1);
         const uint32_t vpar = (uint32_t)((j / VST) & 1);
         if (!mbar_wait(&v_full[vs], vpar, abort, args.err, 0x406, args.wait_ns) ||
             !mbar_wait(&v_ok[vs], vpar, abort, args.err, 0x40C, args.wait_ns)) {
@@ -406,35 +431,29 @@ __global__ void __launch_bounds__(THREADS, 1)
           break;
         }
         const uint32_t va = base + OFF_V + vs * TILE;
-        for (int t = 0; t < QT && ok; ++t) {
-          if (!mbar_wait(&p_full[t], (uint32_t)(j & 1), abort, args.err, 0x405, args.wait_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t pa = tmem + (uint32_t)(t * 256);
-          const uint32_t d = tmem + (uint32_t)(t * 256 + 128);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t db = sw128_desc(va + (uint32_t)kk * 2048u, HALF, 1024);
-            umma_bf16_tmem_a(d, pa + (uint32_t)(kk * 8), db, idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+        for (int t = 0; t < QT; ++t) {
+          if (ok && sees(t, k0)) {
+            ok = mbar_wait(&p_full[t], (uint32_t)((gt[t] - 1) & 1), abort, args.err, 0x405, args.wait_ns);
+            if (ok) {
+              tc_fence_after();
+              const uint32_t pa = tmem + (uint32_t)(t * 256);
+              const uint32_t d = tmem + (uint32_t)(t * 256 + 128);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint64_t db = sw128_desc(va + (uint32_t)kk * 2048u, HALF, 1024);
+                umma_bf16_tmem_a(d, pa + (uint32_t)(kk * 8), db, idesc_o, (pv[t] || kk > 0) ? 1u : 0u);
+              }
+              umma_commit(&o_done[t]);
+              pv[t] = true;
+            }
           }
-          umma_commit(&o_done[t]);
-          if (t == QT - 1) umma_commit(&v_empty[vs]);
-          if (more) {
-            if (t == 0 &&
-                !mbar_wait(&k_full[ks], (uint32_t)(((j + 1) / KST) & 1), abort, args.err, 0x404, args.wait_ns)) {
-              ok = false;
-              break;
-            }
-            // S_t(j+1) overwrites P_t(j): wait until O_t's P V of this tile has completed
-            if (!mbar_wait(&o_done[t], (uint32_t)(j & 1), abort, args.err, 0x40B, args.wait_ns)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            issue_s(t, ks);
-            if (t == QT - 1) umma_commit(&k_empty[ks]);
+          if (ok && t == QT - 1) umma_commit(&v_empty[vs]);
+          if (ok && more) {
+            if (t == 0)
+              ok = mbar_wait(&k_full[ks], (uint32_t)(((j + 1) / KST) & 1), abort, args.err, 0x404, args.wait_ns);
+            if (ok && sees(t, k1)) ok = issue_s(t, ks);
+            if (ok && t == QT - 1) umma_commit(&k_empty[ks]);
           }
         }
       }
@@ -443,17 +462,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_drain(drain, 0, args.wait_ns);
       }
     }
-  } else if (warp == 2) {
-    // ---------------- V made safe ----------------
+  } else if (warp < 4) {
+    // ---------------- V made safe: a half of each tile per warp ----------------
     for (int j = 0; j < T; ++j) {
       const int vs = j % VST;
       if (!__all_sync(0xffffffffu, mbar_wait(&v_full[vs], (uint32_t)((j / VST) & 1), abort, args.err, 0x409, args.wait_ns)))
         break;
       if (!whole(j)) {
-        uint4* p = reinterpret_cast<uint4*>(smem + OFF_V + vs * TILE);
+        uint4* p = reinterpret_cast<uint4*>(smem + OFF_V + vs * TILE + (warp - 2) * HALF);
         bool found = false;
 #pragma unroll 8
-        for (int i = lane; i < TILE / 16; i += 32) {
+        for (int i = lane; i < HALF / 16; i += 32) {
           uint4 x = p[i];
           if (nonfinite16(x.x) | nonfinite16(x.y) | nonfinite16(x.z) | nonfinite16(x.w)) {
             uint32_t* w = &x.x;
@@ -481,6 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t col_s = (uint32_t)(t * 256), col_o = col_s + 128;
     const int h = h_a + t * dh;
     const int row_t = row0 + t * dr;                           // first row of the tile
+    const int my_see0 = t ? see0[1] : see0[0], my_see1 = t ? see1[1] : see1[0];
     const int w_lo = __reduce_max_sync(0xffffffffu, my_lo), w_hi = __reduce_min_sync(0xffffffffu, my_hi);
     // what any row of the warp sees (an empty row, or one past the end: nothing)
     const int any_lo = __reduce_min_sync(0xffffffffu, live && my_hi > my_lo ? my_lo : INT_MAX);
@@ -506,13 +526,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int w_pos0 = my_pos - lane, w_pos1 = w_pos0 + 31;    // positions of the warp's rows
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    int seen = 0;                                              // key tiles of this query tile so far
     for (int j = 0; j < T && ok; ++j) {
+      if (!(tile_at(j) >= my_see0 && tile_at(j) < my_see1)) continue;
       const int key0 = tile_at(j) * BKV;
       const bool masked = !(key0 >= w_lo && key0 + BKV <= w_hi);
       const bool nothing = key0 >= any_hi || key0 + BKV <= any_lo;
       const int lo = my_lo - key0, hi = my_hi - key0;
       const float fq = (float)(my_pos - key0);
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)(j & 1), abort, args.err, 0x407, args.wait_ns))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)(seen & 1), abort, args.err, 0x407, args.wait_ns))) {
         ok = false;
         break;
       }
@@ -576,7 +598,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);   // O, l are 0 then
             l *= alpha;
             m = m_new;
-            if (j > 0) {
+            if (seen > 0) {
               // O_t's previous P V has completed (S_t(j) was issued after it): rescale it
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
@@ -662,87 +684,119 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[t]);
+      ++seen;
     }
     // ---- output ----
-    if (ok && T > 0) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&o_done[t], (uint32_t)((T - 1) & 1), abort, args.err, 0x40A, args.wait_ns))) ok = false;
+    if (ok && seen > 0) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&o_done[t], (uint32_t)((seen - 1) & 1), abort, args.err, 0x40A, args.wait_ns))) ok = false;
       tc_fence_after();
     }
-    const int q_rows = min(BQ, m_.n_q - row_t);                // may be <= 0
+    const int q_rows = min(BQ, m_.n_q - row_t) - quarter * 32;  // of this warp; may be <= 0
     const size_t ld = (size_t)m_.heads * D;
-    const bool have = ok && T > 0 && (l > 0.f || l != l);
+    const bool have = ok && seen > 0 && (l > 0.f || l != l);
     const float inv = have ? 1.f / l : 0.f;
+    const bool parts = args.n_splits > 1;
     if (ok) {
-      // stage the warp's 32 normalised rows in shared memory (the Q and K stages, which
-      // nothing reads any more), then write whole rows; float4 slot q of row i is at q ^ i
-      float4* stage = reinterpret_cast<float4*>(smem + OFF_Q) + (warp - 4) * (32 * 32);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t u[32];
-        if (T > 0) {
-          tmem_ld32(tmem + lane_base + col_o + c * 32, u);
-          tmem_wait_ld(u);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) u[i] = 0u;
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float4 f;
-          f.x = have ? __uint_as_float(u[4 * q]) * inv : 0.f;
-          f.y = have ? __uint_as_float(u[4 * q + 1]) * inv : 0.f;
-          f.z = have ? __uint_as_float(u[4 * q + 2]) * inv : 0.f;
-          f.w = have ? __uint_as_float(u[4 * q + 3]) * inv : 0.f;
-          stage[lane * 32 + ((c * 8 + q) ^ lane)] = f;
-        }
-      }
-      __syncwarp();
-      const bool fix = T > 0 && *dirty != 0;
-      for (int rr = 0; rr < 32; ++rr) {
-        if (quarter * 32 + rr >= q_rows) break;                // warp-uniform
-        float4 f = stage[rr * 32 + (lane ^ rr)];
-        if (fix) {
-          // the non-finite elements of V that this row sees, in the tiles they were taken out of
-          const int lo = __shfl_sync(0xffffffffu, my_lo, rr), hi = __shfl_sync(0xffffffffu, my_hi, rr);
-          for (int j = 0; j < T; ++j) {
-            if (whole(j)) continue;
-            const int k0 = tile_at(j) * BKV, k1 = min(hi, k0 + BKV);
-            for (int k = max(lo, k0); k < k1; ++k) {
-              const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(m_.v) +
-                                                              ((size_t)k * m_.kv_heads + hk) * D + 4 * lane);
-              if (nonfinite16(x.x) || nonfinite16(x.y)) {
-                const float v0 = __uint_as_float(x.x << 16), v1 = __uint_as_float(x.x & 0xffff0000u);
-                const float v2 = __uint_as_float(x.y << 16), v3 = __uint_as_float(x.y & 0xffff0000u);
-                if (!isfinite(v0)) f.x += v0;
-                if (!isfinite(v1)) f.y += v1;
-                if (!isfinite(v2)) f.z += v2;
-                if (!isfinite(v3)) f.w += v3;
-              }
+      // The warp's 32 normalised rows go through shared memory, 256 bytes of each at a time (a
+      // whole bf16 row, or half of a partial's), so that whole lines are written.  The place
+      // is the tile's own Q: its last S was issued before the P V that o_done signalled.  (The
+      // other tile may still be at work on its own Q and on the K and V stages.)  16-byte
+      // piece q of row i is at q ^ (i & 7): no bank conflicts either way.
+      uint4* stage = reinterpret_cast<uint4*>(smem + OFF_Q + t * TILE) + (warp & 3) * (32 * 16);
+      const bool fix = seen > 0 && *dirty != 0;
+      const size_t row_bytes = ld * (parts ? 4 : 2);
+      char* out = (parts ? reinterpret_cast<char*>(args.o_part + (size_t)split * m_.n_q * ld)
+                         : reinterpret_cast<char*>(m_.o)) +
+                  (size_t)(row_t + quarter * 32) * row_bytes + (size_t)h * D * (parts ? 4 : 2) + (lane & 15) * 16;
+      // the non-finite elements of V that row rr of the warp sees in columns [c, c + 4), in the
+      // tiles they were taken out of: the row's sum is then theirs, whatever their weights
+      auto add_back = [&](int rr, int c, float4* f) {
+        const int lo = __shfl_sync(0xffffffffu, my_lo, rr), hi = __shfl_sync(0xffffffffu, my_hi, rr);
+        for (int j = 0; j < T; ++j) {
+          if (whole(j)) continue;
+          const int k0 = tile_at(j) * BKV, k1 = min(hi, k0 + BKV);
+          for (int k = max(lo, k0); k < k1; ++k) {
+            const uint2 x = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(m_.v) +
+                                                            ((size_t)k * m_.kv_heads + hk) * D + c);
+            if (nonfinite16(x.x) || nonfinite16(x.y)) {
+              const float v0 = __uint_as_float(x.x << 16), v1 = __uint_as_float(x.x & 0xffff0000u);
+              const float v2 = __uint_as_float(x.y << 16), v3 = __uint_as_float(x.y & 0xffff0000u);
+              if (!isfinite(v0)) f->x += v0;
+              if (!isfinite(v1)) f->y += v1;
+              if (!isfinite(v2)) f->z += v2;
+              if (!isfinite(v3)) f->w += v3;
             }
           }
         }
-        const size_t at = (size_t)(row_t + quarter * 32 + rr) * ld + (size_t)h * D + 4 * lane;
-        if (args.n_splits == 1) {
-          uint2 b;
-          b.x = pack_bf16x2(f.x, f.y);
-          b.y = pack_bf16x2(f.z, f.w);
-          *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(m_.o) + at) = b;
-        } else {
-          *reinterpret_cast<float4*>(args.o_part + (size_t)split * m_.n_q * ld + at) = f;
+      };
+#pragma unroll 1
+      for (int round = 0; round < (parts ? 2 : 1); ++round) {
+        const int cols = parts ? 64 : 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c * 32 >= cols) break;                           // warp-uniform
+          uint32_t u[32];
+          if (seen > 0) {
+            tmem_ld32(tmem + lane_base + col_o + round * 64 + c * 32, u);
+            tmem_wait_ld(u);
+          }
+          float* f = reinterpret_cast<float*>(u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] = have ? f[i] * inv : 0.f;
+          if (parts) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              stage[lane * 16 + ((c * 8 + q) ^ (lane & 7))] = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              stage[lane * 16 + ((c * 4 + q) ^ (lane & 7))] =
+                  make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
+                             pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
+          }
         }
+        __syncwarp();
+        if (!fix) {
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {
+            const int rr = 2 * i + (lane >> 4);
+            if (rr < q_rows)
+              *reinterpret_cast<uint4*>(out + rr * row_bytes) = stage[rr * 16 + ((lane & 15) ^ (rr & 7))];
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 16; ++i) {
+            const int rr = 2 * i + (lane >> 4);
+            const uint4 x = stage[rr * 16 + ((lane & 15) ^ (rr & 7))];
+            float4 f = *reinterpret_cast<const float4*>(&x);
+            if (parts) {
+              add_back(rr, round * 64 + (lane & 15) * 4, &f);
+              if (rr < q_rows) *reinterpret_cast<float4*>(out + rr * row_bytes) = f;
+              continue;
+            }
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t wa = e ? x.z : x.x, wb = e ? x.w : x.y;
+              f = make_float4(__uint_as_float(wa << 16), __uint_as_float(wa & 0xffff0000u),
+                              __uint_as_float(wb << 16), __uint_as_float(wb & 0xffff0000u));
+              add_back(rr, (lane & 15) * 8 + e * 4, &f);
+              if (rr < q_rows)
+                *reinterpret_cast<uint2*>(out + rr * row_bytes + e * 8) =
+                    make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+            }
+          }
+        }
+        out += 256;
+        __syncwarp();
       }
-    } else if (r < q_rows) {
+    } else if (lane < q_rows) {
       // unwinding after a timed-out wait: zeros, written directly
       const size_t at = (size_t)(row_t + r) * ld + (size_t)h * D;
-      if (args.n_splits == 1) {
-        uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(m_.o) + at);
-        for (int q = 0; q < D / 8; ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
-      } else {
-        float4* d = reinterpret_cast<float4*>(args.o_part + (size_t)split * m_.n_q * ld + at);
-        for (int q = 0; q < D / 4; ++q) d[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      uint4* d = parts ? reinterpret_cast<uint4*>(args.o_part + (size_t)split * m_.n_q * ld + at)
+                       : reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(m_.o) + at);
+      for (int q = 0; q < D / (parts ? 4 : 8); ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
     }
-    if (r < q_rows && args.n_splits > 1)
+    if (lane < q_rows && parts)
       args.lse_part[((size_t)split * m_.n_q + row_t + r) * m_.heads + h] = have ? m + log2f(l) : -INFINITY;
   }
 
