@@ -577,21 +577,25 @@ __global__ void __launch_bounds__(THREADS, 1)
           float mx = -INFINITY;                                // of the visible scores
           // With nothing masked and no bias the bound is itself the largest score, or (cap) as
           // far above it that no score is lost under 2^-126 while it is small.
-          if (!BIAS && !masked && __all_sync(0xffffffffu, !CAP || bound <= 40.f)) mx = bound;
-          else
+          if (!BIAS && !masked && __all_sync(0xffffffffu, !CAP || bound <= 40.f)) {
+            mx = bound;
+          } else {
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t w[16];
-            tmem_ld16(tmem + lane_base + col_s + c * 16, w);
-            tmem_wait_ld(w);
-            const float* sv = reinterpret_cast<const float*>(w);
-            const uint32_t bits = range_bits(lo - c * 16, hi - c * 16);
-            const float fc = fq - (float)(c * 16);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w[32];
+              tmem_ld32(tmem + lane_base + col_s + c * 32, w);
+              tmem_wait_ld(w);
+              const float* sv = reinterpret_cast<const float*>(w);
+              const uint32_t bits = range_bits(lo - c * 32, hi - c * 32);
+              const float fc = fq - (float)(c * 32);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float z = score2<CAP, BIAS>(sm, sv[i], fc, (float)i);
-              if ((bits >> i) & 1u) mx = fmaxf(mx, z);
+              for (int i = 0; i < 32; ++i) {
+                // without a bias the score rises with the product: the largest product does
+                const float z = BIAS ? score2<CAP, BIAS>(sm, sv[i], fc, (float)i) : sv[i];
+                if ((bits >> i) & 1u) mx = fmaxf(mx, z);
+              }
             }
+            if (!BIAS) mx = score2<CAP, BIAS>(sm, mx, 0.f, 0.f);
           }
           if (__any_sync(0xffffffffu, mx > m + kRescaleLog2)) {   // also from m = -inf
             const float m_new = fmaxf(m, mx);
@@ -621,56 +625,68 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool fast = true;
         if (BIAS) fast = side != 0.f && __all_sync(0xffffffffu, fabsf(sm.slope2 * fq) < 16384.f);
         if (CAP) fast = fast && __all_sync(0xffffffffu, top <= sm.x_lim);
+        // The common form is unrolled over all 128 columns, the others over 64: all of them
+        // unrolled do not fit the instruction cache once the warps of a tile are in different
+        // forms (a row short of its neighbours then cost its block 1 us a tile, 3 us capped).
         auto make_p = [&](auto is_masked, auto is_fast) {
           constexpr bool MASKED = decltype(is_masked)::value, FAST = decltype(is_fast)::value;
+          constexpr int ROUNDS = MASKED ? 2 : 1, CHUNKS = 4 / ROUNDS, COLS = 32 * CHUNKS;
           F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
           const float neg_m = m == -INFINITY ? 0.f : -m;
           const float tilt = sm.slope2 * side;                 // z gains tilt (col - fq)
-          const float t0 = BIAS && FAST ? fmaf(-tilt, fq, neg_m) : neg_m;
           uint32_t u[2][32];
           tmem_ld32(tmem + lane_base + col_s, u[0]);
           tmem_wait_ld(u[0]);
+#pragma unroll 1
+          for (int round = 0; round < ROUNDS; ++round) {
+            const float fr = fq - (float)(COLS * round);
+            const float t0 = BIAS && FAST ? fmaf(-tilt, fr, neg_m) : neg_m;
+            const uint32_t src = tmem + lane_base + col_s + (uint32_t)(COLS * round);
+            const uint32_t dst = tmem + lane_base + col_s + (uint32_t)(COLS / 2 * round);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c + 1 < 4) tmem_ld32(tmem + lane_base + col_s + (c + 1) * 32, u[(c + 1) & 1]);
-            const float* sv = reinterpret_cast<const float*>(u[c & 1]);
-            const uint32_t bits = MASKED ? range_bits(lo - c * 32, hi - c * 32) : 0u;
-            uint32_t pk[16];
+            for (int c = 0; c < CHUNKS; ++c) {
+              // (CHUNKS is even: the next round's first chunk goes where this one's did)
+              const bool next = c + 1 < CHUNKS || round + 1 < ROUNDS;
+              if (next) tmem_ld32(src + (c + 1) * 32, u[(c + 1) & 1]);
+              const float* sv = reinterpret_cast<const float*>(u[c & 1]);
+              const uint32_t bits = MASKED ? range_bits(lo - COLS * round - c * 32, hi - COLS * round - c * 32) : 0u;
+              uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              F2 t(t0, t0);
-              if (BIAS) {
-                const float c0 = (float)(c * 32 + 2 * i), c1 = c0 + 1.f;
-                t = FAST ? F2(fmaf(tilt, c0, t0), fmaf(tilt, c1, t0))
-                         : F2(fmaf(-sm.slope2, fabsf(fq - c0), t0), fmaf(-sm.slope2, fabsf(fq - c1), t0));
-              }
-              const float x0 = sv[2 * i], x1 = sv[2 * i + 1];
-              const F2 x(x0, x1);
-              F2 z;
-              if (!CAP) {
-                z = fma2(x, sc2, t);
-              } else if (FAST) {
-                const F2 y2 = mul2(x, x);
-                F2 w = poly[4];
+              for (int i = 0; i < 16; ++i) {
+                F2 t(t0, t0);
+                if (BIAS) {
+                  const float c0 = (float)(c * 32 + 2 * i), c1 = c0 + 1.f;
+                  t = FAST ? F2(fmaf(tilt, c0, t0), fmaf(tilt, c1, t0))
+                           : F2(fmaf(-sm.slope2, fabsf(fr - c0), t0), fmaf(-sm.slope2, fabsf(fr - c1), t0));
+                }
+                const float x0 = sv[2 * i], x1 = sv[2 * i + 1];
+                const F2 x(x0, x1);
+                F2 z;
+                if (!CAP) {
+                  z = fma2(x, sc2, t);
+                } else if (FAST) {
+                  const F2 y2 = mul2(x, x);
+                  F2 w = poly[4];
 #pragma unroll
-                for (int k = 3; k >= 0; --k) w = fma2(w, y2, poly[k]);
-                z = fma2(x, w, t);
-              } else {
-                z = fma2(F2(sm.cap2, sm.cap2), F2(tanh_ex2(x0 * sm.sc), tanh_ex2(x1 * sm.sc)), t);
+                  for (int k = 3; k >= 0; --k) w = fma2(w, y2, poly[k]);
+                  z = fma2(x, w, t);
+                } else {
+                  z = fma2(F2(sm.cap2, sm.cap2), F2(tanh_ex2(x0 * sm.sc), tanh_ex2(x1 * sm.sc)), t);
+                }
+                float p0, p1;
+                z.get(&p0, &p1);
+                if (MASKED) {
+                  if (!((bits >> (2 * i)) & 1u)) p0 = -INFINITY;
+                  if (!((bits >> (2 * i + 1)) & 1u)) p1 = -INFINITY;
+                }
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                sum[i & 1] = add2(sum[i & 1], F2(p0, p1));
+                pk[i] = pack_bf16x2(p0, p1);
               }
-              float p0, p1;
-              z.get(&p0, &p1);
-              if (MASKED) {
-                if (!((bits >> (2 * i)) & 1u)) p0 = -INFINITY;
-                if (!((bits >> (2 * i + 1)) & 1u)) p1 = -INFINITY;
-              }
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              sum[i & 1] = add2(sum[i & 1], F2(p0, p1));
-              pk[i] = pack_bf16x2(p0, p1);
+              if (next) tmem_wait_ld(u[(c + 1) & 1]);
+              tmem_st16(dst + c * 16, pk);
             }
-            if (c + 1 < 4) tmem_wait_ld(u[(c + 1) & 1]);
-            tmem_st16(tmem + lane_base + col_s + c * 16, pk);
           }
           float a0, a1;
           add2(sum[0], sum[1]).get(&a0, &a1);
