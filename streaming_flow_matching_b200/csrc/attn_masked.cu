@@ -49,6 +49,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Query i of document d (starts[d] <= pos < starts[d + 1]): keys from starts[d] up to the
 // document's end, or (causal) up to max(pos + 1, starts[d] + prefix[d]).
 __global__ void __launch_bounds__(256) attention_bounds_kernel(const __grid_constant__ BoundsArgs a) {
+  grid_dependency_wait();
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= a.n_q) return;
   const int pos = a.n_kv - a.n_q + i;
@@ -1175,8 +1176,7 @@ int launch_attention_masked_f32(const MaskedArgs& a, void* workspace, cudaStream
 
 int launch_attention_bounds(const BoundsArgs& a, cudaStream_t s) {
   ProfScope ps(SFM_PROF_ROWOPS, s);
-  attention_bounds_kernel<<<(unsigned)((a.n_q + 255) / 256), 256, 0, s>>>(a);
-  return record_cuda(cudaGetLastError());
+  return record_cuda(launch_dependent(attention_bounds_kernel, (unsigned)((a.n_q + 255) / 256), 256, 0, s, a));
 }
 
 }  // namespace sfm

@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int g0 = (hg - hk * sp.gt) * (8 * NT);                // first query head of the group here
   const int nh = min(8 * NT, G - g0);                         // query heads of this tile
   const int h0 = hk * G + g0;
+  grid_dependency_wait();
   grid_dependency_trigger();                                  // the finishing kernel may be set up
   const int total = total_tiles(a.c, lane, a.err);
   const int chunk = (total + sp.slots - 1) / sp.slots;
@@ -470,6 +471,7 @@ __global__ void __launch_bounds__(kThreads)
   const int g0 = (hg - hk * sp.gt) * GT;
   const int nh = min(GT, G - g0);
   const int h0 = hk * G + g0;
+  grid_dependency_wait();
   grid_dependency_trigger();                                  // the finishing kernel may be set up
   const int total = total_tiles(a.c, lane, a.err);
   const int chunk = (total + sp.slots - 1) / sp.slots;
@@ -866,15 +868,14 @@ cudaError_t launch_bf16(const DecodeArgs& a, const Split& sp, unsigned grid, cud
                     : (bias ? paged_attn_bf16_kernel<NT, false, true> : paged_attn_bf16_kernel<NT, false, false>);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBf16);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, kSmemBf16, s>>>(a, sp);
-  return cudaGetLastError();
+  return launch_dependent(kernel, grid, kThreads, kSmemBf16, s, a, sp);
 }
 
 template <int DV>
-void launch_fp32(const DecodeArgs& a, const Split& sp, unsigned grid, cudaStream_t s) {
-  if (sp.hpt == 4) paged_attn_fp32_kernel<DV, 4><<<grid, kThreads, 0, s>>>(a, sp);
-  else if (sp.hpt == 2) paged_attn_fp32_kernel<DV, 2><<<grid, kThreads, 0, s>>>(a, sp);
-  else paged_attn_fp32_kernel<DV, 1><<<grid, kThreads, 0, s>>>(a, sp);
+cudaError_t launch_fp32(const DecodeArgs& a, const Split& sp, unsigned grid, cudaStream_t s) {
+  if (sp.hpt == 4) return launch_dependent(paged_attn_fp32_kernel<DV, 4>, grid, kThreads, 0, s, a, sp);
+  if (sp.hpt == 2) return launch_dependent(paged_attn_fp32_kernel<DV, 2>, grid, kThreads, 0, s, a, sp);
+  return launch_dependent(paged_attn_fp32_kernel<DV, 1>, grid, kThreads, 0, s, a, sp);
 }
 
 }  // namespace
@@ -896,12 +897,11 @@ int launch_paged_attention(const DecodeArgs& a, int dtype, void* workspace, cuda
       e = sp.hpt == 8 ? launch_bf16<1>(a, sp, grid, s) : launch_bf16<2>(a, sp, grid, s);
     } else {
       switch (a.c.head_dim / 32) {
-        case 1: launch_fp32<1>(a, sp, grid, s); break;
-        case 2: launch_fp32<2>(a, sp, grid, s); break;
-        case 3: launch_fp32<3>(a, sp, grid, s); break;
-        default: launch_fp32<4>(a, sp, grid, s); break;
+        case 1: e = launch_fp32<1>(a, sp, grid, s); break;
+        case 2: e = launch_fp32<2>(a, sp, grid, s); break;
+        case 3: e = launch_fp32<3>(a, sp, grid, s); break;
+        default: e = launch_fp32<4>(a, sp, grid, s); break;
       }
-      e = cudaGetLastError();
     }
     if ((rc = record_cuda(e))) return rc;
   }

@@ -28,6 +28,7 @@ constexpr int kAppendThreads = 256;
 
 __global__ void __launch_bounds__(kAppendThreads)
     paged_append_kernel(const __grid_constant__ AppendArgs a, int row_vecs, int rows_per_cta) {
+  grid_dependency_wait();
   const int r0 = blockIdx.x * rows_per_cta;
   const int rows = min(rows_per_cta, a.n_rows - r0);
   auto place = [&](int r, int* seq, int* i) -> bool {   // row -> sequence and index in it
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictArgs a, int* __restrict__ counts,
                         int* __restrict__ lists, int room, int held) {
   __shared__ SelectShared sh;
+  grid_dependency_wait();
   const int n = cache_len(a.c, blockIdx.x / a.c.kv_heads, a.err);
   if (n <= a.keep) {
     if (threadIdx.x == 0) counts[blockIdx.x] = 0;
@@ -352,8 +354,8 @@ int launch_paged_append(const AppendArgs& a, int row_bytes, cudaStream_t s) {
   int rows = 2 * kAppendThreads / row_vecs;
   rows = rows < 1 ? 1 : rows > 16 ? 16 : rows;
   ProfScope ps(SFM_PROF_APPEND, s);
-  paged_append_kernel<<<(unsigned)((a.n_rows + rows - 1) / rows), kAppendThreads, 0, s>>>(a, row_vecs, rows);
-  return record_cuda(cudaGetLastError());
+  return record_cuda(launch_dependent(paged_append_kernel, (unsigned)((a.n_rows + rows - 1) / rows), kAppendThreads, 0,
+                                      s, a, row_vecs, rows));
 }
 
 // Rows moved per (sequence, key head): at most the slots past `keep`, and at most `keep`.
@@ -379,8 +381,8 @@ int launch_paged_evict(const EvictArgs& a, int row_bytes_head, void* workspace, 
   const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kHeldRanks * (int)sizeof(unsigned));
   if (e != cudaSuccess) return record_cuda(e);
-  evict_select_kernel<<<(unsigned)items, kSelThreads, held * sizeof(unsigned), s>>>(a, counts, lists, room, held);
-  int rc = record_cuda(cudaGetLastError());
+  int rc = record_cuda(launch_dependent(evict_select_kernel, (unsigned)items, kSelThreads, held * sizeof(unsigned), s, a,
+                                        counts, lists, room, held));
   if (rc) return rc;
   // kMoveRows rows per warp, and no more CTAs than fill the device several times over
   int blocks = (room + kMoveRows * kMoveWarps - 1) / (kMoveRows * kMoveWarps);
