@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float scale = 0.08838834764831845f;                   // 1 / sqrt(128)
   const float inv_cap = CAP ? 1.f / a.softcap : 0.f;
   int q_pos = 0;
+  float* score_rows = nullptr;                                // of head 2 t4 of the tile
   bool seg_start = false;
 
   for (int it = 0; it < n_tiles; ++it) {
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
       }
       if (BIAS) q_pos = a.q_positions ? __ldg(a.q_positions + cw.seq) : cw.len - 1;
+      if (sp.scores) score_rows = sp.scores + ((size_t)cw.seq * a.heads + h0 + 2 * t4) * sp.pitch;
     }
     // keep the ring full: the tile kStages - 1 ahead goes where the last one was consumed
     if (it + kStages - 1 < n_tiles) {
@@ -322,14 +324,21 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       if (sp.scores) {
         // raw scores for the pass that accumulates weights: 8 consecutive tokens per head
+        float* sc = score_rows + tok;
+        const bool w0 = tok < cw.len, w1 = tok + 8 < cw.len;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int hh = nt * 8 + 2 * t4 + (e & 1), tt = tok + (e >= 2 ? 8 : 0);
-            if (hh < nh && tt < cw.len)
-              sp.scores[((size_t)cw.seq * a.heads + h0 + hh) * sp.pitch + tt] = s[nt][e];
+        for (int nt = 0; nt < NT; ++nt) {
+          const int hh = nt * 8 + 2 * t4;
+          if (hh < nh) {
+            if (w0) sc[0] = s[nt][0];
+            if (w1) sc[8] = s[nt][2];
           }
+          if (hh + 1 < nh) {
+            if (w0) sc[sp.pitch] = s[nt][1];
+            if (w1) sc[sp.pitch + 8] = s[nt][3];
+          }
+          sc += 8 * (size_t)sp.pitch;
+        }
       }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -718,7 +727,8 @@ __device__ void join_ml(const Split& sp, int G, int h, const Parts& p, int lane,
   *l = sum;
 }
 
-constexpr int kFinThreads = 256, kFinWarps = kFinThreads / 32, kAccTok = 2048;
+constexpr int kFinThreads = 256, kAccTok = 1024;
+constexpr int kTokThread = kAccTok / kFinThreads, kHeadsOnce = 4;
 
 // The finishing kernel.  Its first CTAs join, one per (sequence, query head): a sequence
 // finished by one CTA is left alone, an empty one gets zeros; the partials are summed in a
@@ -730,7 +740,7 @@ template <typename T>
 __global__ void __launch_bounds__(kFinThreads)
     paged_finish_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp, int blocks_per_item) {
   __shared__ float4 buf[kFinThreads];
-  __shared__ float2 sh[kFinWarps];
+  __shared__ float sh[kHeadsOnce];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.heads / a.c.kv_heads;
   if ((int)blockIdx.x < sp.joins) {
@@ -780,42 +790,53 @@ __global__ void __launch_bounds__(kFinThreads)
     return;
   }
   const Parts p = find_parts(a.c, sp, seq, lane);
-  grid_dependency_wait();
-  const float* sc = sp.scores + ((size_t)seq * a.heads + hk * G) * sp.pitch;
   float* w = a.weights + (size_t)item * a.cap;
-  float add[kAccTok / kFinThreads];
+  float add[kTokThread];                                       // the slots' weights so far
 #pragma unroll
-  for (int i = 0; i < kAccTok / kFinThreads; ++i) add[i] = 0.f;
-  for (int g0 = 0; g0 < G; g0 += kFinWarps) {
-    if (g0 + warp < G) {
+  for (int i = 0; i < kTokThread; ++i) {
+    const int t = blk * kAccTok + i * kFinThreads + tid;
+    add[i] = t < t1 ? w[t] : 0.f;
+  }
+  grid_dependency_wait();
+  const float* sc = sp.scores + ((size_t)seq * a.heads + hk * G) * sp.pitch + blk * kAccTok + tid;
+  float step[kTokThread];
+#pragma unroll
+  for (int i = 0; i < kTokThread; ++i) step[i] = 0.f;
+  for (int g0 = 0; g0 < G; g0 += kHeadsOnce) {
+    // the scores of a few heads are on their way while their log-sum-exps are made, a warp each
+    float s[kHeadsOnce][kTokThread];
+#pragma unroll
+    for (int x = 0; x < kHeadsOnce; ++x)
+#pragma unroll
+      for (int i = 0; i < kTokThread; ++i) {
+        const int t = blk * kAccTok + i * kFinThreads + tid;
+        s[x][i] = g0 + x < G && t < t1 ? __ldcg(sc + (size_t)(g0 + x) * sp.pitch + i * kFinThreads) : -INFINITY;
+      }
+    if (warp < kHeadsOnce && g0 + warp < G) {
       const int h = hk * G + g0 + warp;
       float m, l;
       if (p.s0 == p.s1) {                                      // the attention kernel left it whole
         m = __ldcg(sp.lse + (size_t)seq * a.heads + h);
-        l = 1.f;
       } else {
         join_ml(sp, G, h, p, lane, &m, &l);
         m += log2f(l);
       }
-      if (lane == 0) sh[warp] = make_float2(m, l);
+      if (lane == 0) sh[warp] = m;
     }
     __syncthreads();
-    const int ng = min(kFinWarps, G - g0);
-    for (int gi = 0; gi < ng; ++gi) {
-      const float ls = sh[gi].x;
+#pragma unroll
+    for (int x = 0; x < kHeadsOnce; ++x) {
+      const float ls = g0 + x < G ? sh[x] : -INFINITY;
       if (ls == -INFINITY) continue;                           // no visible slot (every page bad)
 #pragma unroll
-      for (int i = 0; i < kAccTok / kFinThreads; ++i) {
-        const int t = blk * kAccTok + i * kFinThreads + tid;
-        if (t < t1) add[i] += ex2_approx(sc[(size_t)(g0 + gi) * sp.pitch + t] - ls);
-      }
+      for (int i = 0; i < kTokThread; ++i) step[i] += ex2_approx(s[x][i] - ls);
     }
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < kAccTok / kFinThreads; ++i) {
+  for (int i = 0; i < kTokThread; ++i) {
     const int t = blk * kAccTok + i * kFinThreads + tid;
-    if (t < t1) w[t] += add[i];
+    if (t < t1) w[t] = add[i] + step[i];
   }
 }
 
