@@ -408,7 +408,8 @@ SFM_API int sfm_fm_solve_exact_velocity(const sfm_handle* h, const float* z0, fl
  * scores and a distance bias.  The thinker's token-causal language / state pass
  * ("Wan-Streamer" v0.2 blog, "Infra") over several sessions packed into one
  * call is its use here; the pages give no formula for it.
- *   s_ij = q_i . k_j / sqrt(D_h);  s = softcap tanh(s / softcap) if softcap > 0;
+ *   s_ij = q_i . k_j / sqrt(D_h);  s = softcap tanh(s / softcap) if softcap > 0
+ *   (0, or in [1e-3, 1e30]: SFM_EINVAL otherwise);
  *   s -= slopes[h] |n_kv - n_q + i - j| if slopes;
  *   o_i = sum_j softmax_j(s_ij) v_j over key_lo[i] <= j < key_hi[i]
  * q, o: [n_q][n_heads][D_h]; k, v: [n_kv][n_kv_heads][D_h], n_heads a multiple of

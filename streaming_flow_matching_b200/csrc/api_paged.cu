@@ -50,6 +50,9 @@ int fill_cache(PagedCache* c, const void* k_pages, const void* v_pages, const in
   return SFM_OK;
 }
 
+// 0 (none), or a cap whose powers and multiples the kernels' fp32 constants hold
+bool cap_ok(float c) { return c == 0.f || (c >= 1e-3f && c <= 1e30f); }
+
 // grids are one-dimensional: every launch's block count has to fit
 bool fits_grid(long long blocks) { return blocks >= 1 && blocks <= INT_MAX; }
 
@@ -104,7 +107,7 @@ int sfm_paged_attention(const void* q, const void* k_pages, const void* v_pages,
   int rc = check_heads(n_heads, n_kv_heads, head_dim, dtype);
   if (rc) return rc;
   if (!q || !o || o == q || !aligned(q, 16) || !aligned(o, 16)) return SFM_EINVAL;
-  if (!(softcap >= 0.f) || isinf(softcap)) return SFM_EINVAL;
+  if (!cap_ok(softcap)) return SFM_EINVAL;
   const bool state = positions || weights;
   if ((state && cap < 1) || ((positions != nullptr) != (q_positions != nullptr)) || (positions && !slopes))
     return SFM_EINVAL;
@@ -114,8 +117,8 @@ int sfm_paged_attention(const void* q, const void* k_pages, const void* v_pages,
   rc = fill_cache(&a.c, k_pages, v_pages, table, lengths, n_seq, n_pages, page_size, max_pages, n_kv_heads,
                   head_dim, state ? cap : -1);
   if (rc) return rc;
-  if (!fits_grid((long long)n_seq * n_heads) ||
-      !fits_grid((long long)n_seq * n_kv_heads * (a.c.max_tokens / 1024 + 1)))
+  if (!fits_grid((long long)n_seq * n_heads) || !fits_grid((long long)n_seq * n_kv_heads) ||
+      !fits_grid((long long)n_seq * n_heads + (long long)n_seq * n_kv_heads * (a.c.max_tokens / 1024 + 1)))
     return SFM_EUNSUPPORTED;
   const size_t need =
       paged_attention_workspace(n_seq, a.c.max_tokens, n_heads, n_kv_heads, head_dim, dtype, weights != nullptr);
@@ -196,7 +199,7 @@ int sfm_attention_masked(const void* q, const void* k, const void* v, void* o, i
   if (rc) return rc;
   if (!q || !k || !v || !o || o == q || n_q < 1 || n_kv < 1) return SFM_EINVAL;
   if (slopes && n_kv < n_q) return SFM_EINVAL;      // the bias needs the queries' positions among the keys
-  if (!(softcap >= 0.f) || isinf(softcap)) return SFM_EINVAL;
+  if (!cap_ok(softcap)) return SFM_EINVAL;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(key_lo, 4) ||
       !aligned(key_hi, 4) || !aligned(slopes, 4))
     return SFM_EINVAL;

@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
     const int seq = cw.seq;
     const bool seq_done = (cw.tile + 1) * kTile >= cw.len;
-    cw.next(a.c);
+    if (it + 1 < n_tiles) cw.next(a.c);
     if (!seq_done && it + 1 < n_tiles) continue;
 
     // ---- the sequence, or the run, ends here: merge the four warps
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     const int base = cw.tile * kTile + warp * kWarpTok;
     Walk nw = cw;
-    nw.next(a.c);
+    if (b + 1 < b1) nw.next(a.c);
     const int next16 = b + 1 < b1 ? lookup(nw) : -1;
 #pragma unroll
     for (int step = 0; step < kWarpTok / 4; ++step) {
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kThreads)
     row16 = next16;
     const int seq = cw.seq;
     const bool seq_done = (cw.tile + 1) * kTile >= cw.len;
-    cw.next(a.c);
+    cw = nw;
     if (!seq_done && b + 1 < b1) continue;
 
     fresh = true;

@@ -176,6 +176,11 @@ def test_key_splits_join(cuda_device, dtype, d, n_q, n_kv, h, hk):
     out = run(q, k, v, None, hi)
     if n_q > 2:
         assert int(torch.count_nonzero(out[2])) == 0
+    k[n_kv - 700:], v[n_kv - 700:] = float("nan"), float("inf")
+    v[50, 0, 1] = float("-inf")
+    hi = ints([n_kv - 700 - 300 * (i % 4) for i in range(n_q)])
+    lo = ints([60 * (i % 2) for i in range(n_q)])
+    run(q, k, v, lo, hi)
 
 
 @pytest.mark.parametrize("h,hk", [(1, 1), (3, 1), (4, 2)])
@@ -217,6 +222,12 @@ def test_large_scores(cuda_device):
     k = (k.float() * torch.linspace(1, 40, n, device="cuda")[:, None, None]).to(BF)
     run(q, k, v)
     run(q, k, v, softcap=50.0)
+    # caps far from the scores on either side, slopes that favour far keys
+    run(q, k, v, softcap=1000.0)
+    run(q, k, v, softcap=1e-3)
+    run(q, k, v, softcap=1e20)
+    run(q, k, v, slopes=-0.05 * ladder(2))
+    run(q, k, v, slopes=-0.05 * ladder(2), softcap=5.0)
 
 
 def test_infinite_scores(cuda_device):

@@ -191,7 +191,7 @@ def test_attention_lengths_and_heads(cuda_device, dtype, d, page, h, hk):
 
 
 @pytest.mark.parametrize("dtype,d,h,hk,lens", [
-    (BF, 128, 24, 8, [5000, 17, 3000, 1, 900]), (BF, 128, 4, 4, [20000]), (BF, 128, 16, 1, [7001, 7002]),
+    (BF, 128, 24, 8, [5000, 17, 3000, 1, 900]), (BF, 128, 4, 4, [20000]), (BF, 128, 16, 1, [7001, 7002]), (BF, 128, 300, 1, [500, 3]),
     (F32, 64, 8, 2, [4000, 10, 2500]), (BF, 128, 300, 300, [100, 65])])
 @pytest.mark.parametrize("cap,bias", [(0.0, False), (0.0, True), (30.0, False), (30.0, True)])
 def test_attention_splits(cuda_device, dtype, d, h, hk, lens, cap, bias):
@@ -215,6 +215,8 @@ def test_attention_positions(cuda_device, dtype, d):
     pos = torch.stack([torch.stack([torch.randperm(705, device="cuda") * 3 for _ in range(hk)]) for _ in lens])
     pos = pos.to(torch.int32).contiguous()
     run(c, q, lens, slopes=ladder(h), positions=pos, q_positions=ints([2200, 0, 5]))
+    run(c, q, lens, slopes=-0.01 * ladder(h), softcap=1000.0)
+    run(c, q, lens, softcap=1e-3)
     run(c, q, lens, slopes=ladder(h), positions=pos, q_positions=ints([2200, 0, 5]), softcap=10.0,
         weights=torch.zeros(3, hk, 705, device="cuda"))
 
@@ -227,6 +229,12 @@ def test_attention_many_sequences(cuda_device):
     q = torch.randn(150, 4, 128, device="cuda").to(BF)
     run(c, q, lens, weights=torch.zeros(150, 2, 200, device="cuda"))
     run(c, q, [0] * 150)
+    lens = [0] * 5000
+    lens[3], lens[4000], lens[4999] = 700, 65, 1             # long runs of empty ones
+    c = Cache(lens, 16, 1, 128, BF, seed=3)
+    run(c, torch.randn(5000, 2, 128, device="cuda").to(BF), lens)
+    c = Cache(lens, 16, 1, 32, F32, seed=3)
+    run(c, torch.randn(5000, 2, 32, device="cuda"), lens)
 
 
 def test_attention_unused_rows_may_hold_anything(cuda_device):

@@ -67,7 +67,7 @@ def test_append_arguments(bad):
 
 @pytest.mark.parametrize("bad", [
     dict(q=None), dict(o=None), dict(o=P), dict(q=P + 8), dict(o=P + 2), dict(h=3), dict(h=0), dict(cap=-1.0),
-    dict(cap=INF),
+    dict(cap=INF), dict(cap=1e-4), dict(cap=1e31),
     dict(cap=NAN), dict(positions=None), dict(q_positions=None), dict(slopes=None), dict(room=0), dict(ws=None),
     dict(ws=P + 8), dict(ws_bytes=16), dict(slopes=P + 2)])
 def test_attention_arguments(bad):
@@ -86,7 +86,7 @@ def test_evict_arguments(bad):
     (dict(o=None), L.SFM_EINVAL), (dict(o=P), L.SFM_EINVAL), (dict(n_q=0), L.SFM_EINVAL), (dict(n_kv=0), L.SFM_EINVAL),
     (dict(h=3), L.SFM_EINVAL), (dict(hk=0), L.SFM_EINVAL), (dict(dtype=3), L.SFM_EINVAL),
     (dict(d=64), L.SFM_EUNSUPPORTED), (dict(d=33, dtype=F32), L.SFM_EUNSUPPORTED),
-    (dict(cap=-0.5), L.SFM_EINVAL), (dict(cap=NAN), L.SFM_EINVAL), (dict(cap=INF), L.SFM_EINVAL),
+    (dict(cap=-0.5), L.SFM_EINVAL), (dict(cap=1e-9), L.SFM_EINVAL), (dict(cap=NAN), L.SFM_EINVAL), (dict(cap=INF), L.SFM_EINVAL),
     (dict(n_q=9), L.SFM_EINVAL),                              # a bias needs n_kv >= n_q
     (dict(q=P + 2), L.SFM_EINVAL), (dict(lo=P + 2), L.SFM_EINVAL), (dict(slopes=P + 1), L.SFM_EINVAL),
     (dict(n_q=1, n_kv=4096, ws=None), L.SFM_EINVAL), (dict(n_q=1, n_kv=4096, ws_bytes=64), L.SFM_EINVAL),
