@@ -629,12 +629,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool fast = true;
         if (BIAS) fast = side != 0.f && __all_sync(0xffffffffu, fabsf(sm.slope2 * fq) < 16384.f);
         if (CAP) fast = fast && __all_sync(0xffffffffu, top <= sm.x_lim);
-        // The common form is unrolled over all 128 columns, the others over 64: all of them
-        // unrolled do not fit the instruction cache once the warps of a tile are in different
-        // forms (a row short of its neighbours then cost its block 1 us a tile, 3 us capped).
+        // The common form is unrolled over all 128 columns, the others (and all with a bias) over
+        // 64: unrolled further they do not fit the instruction cache once the warps of a tile are
+        // in different forms (a row short of its neighbours then cost its block 1 us a tile, 3 us
+        // capped).
         auto make_p = [&](auto is_masked, auto is_fast) {
           constexpr bool MASKED = decltype(is_masked)::value, FAST = decltype(is_fast)::value;
-          constexpr int ROUNDS = MASKED ? 2 : 1, CHUNKS = 4 / ROUNDS, COLS = 32 * CHUNKS;
+          constexpr int ROUNDS = MASKED || BIAS ? 2 : 1, CHUNKS = 4 / ROUNDS, COLS = 32 * CHUNKS;
           F2 sum[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
           const float neg_m = m == -INFINITY ? 0.f : -m;
           const float tilt = sm.slope2 * side;                 // z gains tilt (col - fq)

@@ -183,6 +183,19 @@ def test_key_splits_join(cuda_device, dtype, d, n_q, n_kv, h, hk):
     run(q, k, v, lo, hi)
 
 
+@pytest.mark.parametrize("h,hk", [(16, 16), (16, 8)])
+def test_more_blocks_than_sms(cuda_device, h, hk):
+    # several waves of query blocks: all keys, few, none
+    n = 3000
+    q, k, v = make(n, n, h, hk, 128, BF, seed=h + hk)
+    run(q, k, v)
+    hi = ints([n if i % 200 < 100 else 0 if i < 600 else 130 if i < 900 else i + 1 for i in range(n)])
+    out = run(q, k, v, None, hi, softcap=20.0, slopes=ladder(h))
+    assert int(torch.count_nonzero(out[100:200])) == 0
+    out = run(q, k, v, None, ints([min(i, 400) for i in range(n)]))
+    assert int(torch.count_nonzero(out[0])) == 0
+
+
 @pytest.mark.parametrize("h,hk", [(1, 1), (3, 1), (4, 2)])
 @pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, True)])
 def test_query_tiles_with_their_own_keys(cuda_device, h, hk, cap, bias):
