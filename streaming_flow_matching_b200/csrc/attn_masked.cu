@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               pv[t] = true;
             }
           }
-          if (ok && t == QT - 1) umma_commit(&v_empty[vs]);
+          if (ok && more && t == QT - 1) umma_commit(&v_empty[vs]);   // (nothing waits for the last)
           if (ok && more) {
             if (t == 0)
               ok = mbar_wait(&k_full[ks], (uint32_t)(((j + 1) / KST) & 1), abort, args.err, 0x404, args.wait_ns);

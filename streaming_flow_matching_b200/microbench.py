@@ -7,6 +7,8 @@
   python -m streaming_flow_matching_b200.microbench linear --m 924 --n 12288 --k 3072 [--epilogue gelu]
   python -m streaming_flow_matching_b200.microbench step [--layers 1 --cache-units 4]
   python -m streaming_flow_matching_b200.microbench guided --cache-units 48 [--steps 4 --scale 5]
+  python -m streaming_flow_matching_b200.microbench paged --sequences 16 --tokens 8000 [--heads 24 --kv-heads 8]
+  python -m streaming_flow_matching_b200.microbench masked --n-q 8192 [--documents 8 --softcap 50]
   python -m streaming_flow_matching_b200.microbench sweep      # attention + append sweep
 
 Inputs are seeded and larger than L2 where the case allows; each timing is
@@ -29,7 +31,8 @@ if ROOT not in sys.path:
 
 import sfm_synth as S  # noqa: E402
 from streaming_flow_matching_b200 import (Performer, attention, attention_workspace_bytes,  # noqa: E402
-                                          euler_update, linear)
+                                          attention_bounds, attention_masked, euler_update, linear,
+                                          paged_append, paged_attention, paged_evict)
 
 
 def _peaks():
@@ -229,10 +232,55 @@ def bench_units(layers, cache_units, n_units, warmup, reps):
             "ms": ms, "tflops": flop / (ms / 1e3) / 1e12}
 
 
+def bench_paged(n_seq, tokens, heads, kv_heads, warmup, reps, page=64):
+    """One decode step of n_seq sequences of `tokens` cached tokens: append, attention with
+    accumulated weights; and an eviction of a tenth of the cache."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    per = -(-(tokens + 1) // page)
+    shape = (n_seq * per, page, kv_heads, 128)
+    k, v = (torch.randn(shape, generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.randperm(n_seq * per, generator=g, device="cuda").to(torch.int32).view(n_seq, per)
+    before = torch.full((n_seq,), tokens, dtype=torch.int32, device="cuda")
+    after = before + 1
+    w = torch.rand((n_seq, kv_heads, tokens + 1), generator=g, device="cuda")
+    pos = torch.arange(tokens + 1, device="cuda", dtype=torch.int32).expand(w.shape).contiguous()
+    q = torch.randn((n_seq, heads, 128), generator=g, device="cuda").bfloat16()
+    new = torch.randn((n_seq, kv_heads, 128), generator=g, device="cuda").bfloat16()
+    hbm, _, src = _peaks()
+    t_app = _time(lambda: paged_append(new, new, k, v, table, before, positions=pos, weights=w), warmup, reps)
+    t_att = _time(lambda: paged_attention(q, k, v, table, after), warmup, reps)
+    t_wts = _time(lambda: paged_attention(q, k, v, table, after, weights=w), warmup, reps)
+    keep = max(1, tokens - tokens // 10)
+    t_evi = _time(lambda: paged_evict(k, v, table, after, w, pos, keep), warmup, reps)
+    gbs = n_seq * (tokens + 1) * kv_heads * 512 / t_att / 1e6
+    return {"case": "paged", "sequences": n_seq, "tokens": tokens, "heads": heads, "kv_heads": kv_heads,
+            "append_ms": t_app, "attention_ms": t_att, "attention_weights_ms": t_wts, "evict_tenth_ms": t_evi,
+            "attention_gbs": gbs, "of_hbm": gbs / hbm, "peak": src}
+
+
+def bench_masked(n_q, documents, heads, kv_heads, softcap, warmup, reps):
+    """Causal attention of n_q packed tokens in equal documents."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q = torch.randn((n_q, heads, 128), generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn((n_q, kv_heads, 128), generator=g, device="cuda").bfloat16() for _ in range(2))
+    starts = torch.tensor([n_q * d // documents for d in range(documents + 1)], dtype=torch.int32, device="cuda")
+    lo, hi = attention_bounds(n_q, n_q, doc_starts=starts, causal=True)
+    t = _time(lambda: attention_masked(q, k, v, lo, hi, softcap=softcap), warmup, reps)
+    tflops = 4 * 128 * heads * float((hi - lo).sum()) / t / 1e9
+    _, peak, src = _peaks()
+    return {"case": "masked", "n_q": n_q, "documents": documents, "heads": heads, "kv_heads": kv_heads,
+            "softcap": softcap, "ms": t, "tflops_of_visible_pairs": tflops, "of_bf16": tflops / peak, "peak": src}
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["attention", "append", "euler", "linear", "step", "guided",
-                                    "units", "sweep"])
+                                    "units", "paged", "masked", "sweep"])
+    ap.add_argument("--sequences", type=int, default=16)
+    ap.add_argument("--tokens", type=int, default=8000)
+    ap.add_argument("--kv-heads", type=int, default=8)
+    ap.add_argument("--documents", type=int, default=1)
+    ap.add_argument("--softcap", type=float, default=0.0)
     ap.add_argument("--cache-units", type=int, default=4)
     ap.add_argument("--m", type=int, default=924)
     ap.add_argument("--k", type=int, default=3072)
@@ -264,6 +312,10 @@ def main():
         out.append(bench_step(a.layers, a.cache_units, a.warmup, a.reps))
     elif a.case == "guided":
         out.append(bench_guided(a.layers, a.cache_units, a.steps, a.scale, a.warmup, a.reps))
+    elif a.case == "paged":
+        out.append(bench_paged(a.sequences, a.tokens, a.heads, a.kv_heads, a.warmup, a.reps))
+    elif a.case == "masked":
+        out.append(bench_masked(a.n_q, a.documents, a.heads, a.kv_heads, a.softcap, a.warmup, a.reps))
     elif a.case == "units":
         out.append(bench_units(a.layers, a.cache_units, a.units, a.warmup, a.reps))
     else:

@@ -228,6 +228,22 @@ def test_all_keys_equals_attention_in_value(cuda_device):
     assert rel_l2(b.cpu().numpy(), a.cpu().numpy()) <= 2.0 ** -7
 
 
+def test_far_keys(cuda_device):
+    # element offsets past 2^31 in K and V
+    from streaming_flow_matching_b200 import attention_masked
+    n, hk, far = 1100000, 16, 1098500
+    q, _, _ = make(40, 1, hk, hk, 128, BF)
+    k, v = (torch.zeros(n, hk, 128, dtype=BF, device="cuda") for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k[far:] = torch.randn(n - far, hk, 128, generator=g, device="cuda").to(BF)
+    v[far:] = torch.randn(n - far, hk, 128, generator=g, device="cuda").to(BF)
+    v[far + 3, 15, 7] = float("inf")
+    out = attention_masked(q, k, v, ints([far + i for i in range(40)]), ints([n - i for i in range(40)]))
+    ref, mag, _ = R.attend(q, k[far:], v[far:], ints(list(range(40))), ints([n - far - i for i in range(40)]))
+    check(out, ref, mag, BF)
+    assert L.check_call_error() == 0
+
+
 def test_large_scores(cuda_device):
     # scores of hundreds, rising along the keys: the running max moves in every tile
     n = 700
