@@ -393,6 +393,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
+    } else if (sp.scores) {
+      // past the sequence's end, or all on bad pages: the pass after this reads the latter
+      for (int x = lane; x < nh * kWarpTok; x += 32) {
+        const int t = cw.tile * kTile + warp * kWarpTok + (x & (kWarpTok - 1));
+        if (t < cw.len)
+          sp.scores[((size_t)cw.seq * a.heads + h0 + x / kWarpTok) * sp.pitch + t] = -INFINITY;
+      }
     }
     __syncwarp();                                             // the stage may be refilled
 #pragma unroll

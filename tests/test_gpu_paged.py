@@ -278,6 +278,29 @@ def test_attention_bad_pages_and_lengths(cuda_device):
         assert torch.equal(out, good)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_weights_of_slots_on_a_bad_page_stay(cuda_device, dtype, d):
+    # all 16 slots that a warp takes lie on the bad page; the workspace holds anything
+    from streaming_flow_matching_b200 import paged_attention
+    c = Cache([100, 64], 16, 2, d, dtype, seed=7)
+    q = torch.randn(2, 8, d, device="cuda").to(dtype)
+    keep = torch.tensor([t for t in range(100) if not 32 <= t < 48], device="cuda")
+    k, v = c.gather(0, 100)
+    ref, mag, wts = R.attend(q[:1], k[keep], v[keep], ints([0]), ints([84]))
+    t = c.table.clone()
+    t[0, 2] = -1
+    need = L.lib.sfm_paged_attention_workspace_bytes(2, 100, 8, 2, d, 0 if dtype == BF else 1, 1)
+    for fill in (0x41, 0x7f, 0xff):                          # 12.1, 3.4e38, NaN
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        w = torch.full((2, 2, 100), 0.25, device="cuda")
+        out = paged_attention(q, c.k, c.v, t, ints([100, 64]), weights=w, workspace=ws)
+        assert L.check_call_error() == 0x301
+        check_out(out[:1], ref, mag, dtype)
+        assert bool((w[0, :, 32:48] == 0.25).all())
+        err = (w[0, :, keep].double() - 0.25 - wts).abs()
+        assert bool((err <= 5e-4 * wts + 2.0 ** -23 * (0.25 + wts) + 8 * 2.0 ** -126).all())
+
+
 def test_attention_shared_pages_and_infinities(cuda_device):
     from streaming_flow_matching_b200 import paged_attention
     c = Cache([64, 64], 16, 1, 128, BF, seed=8)
