@@ -730,14 +730,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool have = ok && seen > 0 && (l > 0.f || l != l);
     const float inv = have ? 1.f / l : 0.f;
     const bool parts = args.n_splits > 1;
-    if (ok) {
+    if (ok && seen > 0) {
       // The warp's 32 normalised rows go through shared memory, 256 bytes of each at a time (a
       // whole bf16 row, or half of a partial's), so that whole lines are written.  The place
       // is the tile's own Q: its last S was issued before the P V that o_done signalled.  (The
       // other tile may still be at work on its own Q and on the K and V stages.)  16-byte
       // piece q of row i is at q ^ (i & 7): no bank conflicts either way.
       uint4* stage = reinterpret_cast<uint4*>(smem + OFF_Q + t * TILE) + (warp & 3) * (32 * 16);
-      const bool fix = seen > 0 && *dirty != 0;
+      const bool fix = *dirty != 0;
       const size_t row_bytes = ld * (parts ? 4 : 2);
       char* out = (parts ? reinterpret_cast<char*>(args.o_part + (size_t)split * m_.n_q * ld)
                          : reinterpret_cast<char*>(m_.o)) +
@@ -770,10 +770,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 0; c < 4; ++c) {
           if (c * 32 >= cols) break;                           // warp-uniform
           uint32_t u[32];
-          if (seen > 0) {
-            tmem_ld32(tmem + lane_base + col_o + round * 64 + c * 32, u);
-            tmem_wait_ld(u);
-          }
+          tmem_ld32(tmem + lane_base + col_o + round * 64 + c * 32, u);
+          tmem_wait_ld(u);
           float* f = reinterpret_cast<float*>(u);
 #pragma unroll
           for (int i = 0; i < 32; ++i) f[i] = have ? f[i] * inv : 0.f;
@@ -824,7 +822,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
       }
     } else if (lane < q_rows) {
-      // unwinding after a timed-out wait: zeros, written directly
+      // No row of the tile sees a key (its Q may still be landing: no place to stage), or
+      // unwinding after a timed-out wait: zeros, written directly.
       const size_t at = (size_t)(row_t + r) * ld + (size_t)h * D;
       uint4* d = parts ? reinterpret_cast<uint4*>(args.o_part + (size_t)split * m_.n_q * ld + at)
                        : reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(m_.o) + at);

@@ -164,6 +164,31 @@ def test_arbitrary_ranges(cuda_device, dtype, d):
     run(q, k, v, ints([5] * n_q), ints([5] * n_q))          # every range empty
 
 
+@pytest.mark.parametrize("h,hk", [(8, 2), (2, 2)])
+@pytest.mark.parametrize("n_q,n_kv", [(300, 5000), (20000, 20000)])
+def test_empty_blocks_write_zeros_whatever_q_holds(cuda_device, h, hk, n_q, n_kv):
+    # blocks and query tiles without a key: nothing of Q, which is on its way then, may show
+    from streaming_flow_matching_b200 import attention_masked
+    q, k, v = make(n_q, n_kv, h, hk, 128, torch.bfloat16, seed=8)
+    i = torch.arange(n_q, device="cuda", dtype=torch.int32)
+    live = (i // 128) % 5 == 2                               # every fifth tile of 128 rows sees 3 keys
+    hi = torch.where(live, 7, 4).to(torch.int32)
+    lo = torch.full_like(hi, 4)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    seen = v[4:7].double().repeat_interleave(h // hk, 1)
+    for qq in (q, torch.full_like(q, float("nan"))):
+        flush.zero_()
+        out = attention_masked(qq, k, v, lo, hi)
+        assert int(torch.count_nonzero(out[~live])) == 0
+    q0 = torch.zeros_like(q)                                 # equal weights: the mean of the three
+    out = attention_masked(q0, k, v, lo, hi)
+    assert int(torch.count_nonzero(out[~live])) == 0
+    # P is 1, exact in bf16: the output's rounding, and a few of fp32 in the sum and its division
+    tol = seen.mean(0).abs() * 2.0 ** -8 + seen.abs().sum(0) * 2.0 ** -21
+    assert bool(((out[live].double() - seen.mean(0)).abs() <= tol).all())
+    assert L.check_call_error() == 0
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 32), (F32, 96), (F32, 128)])
 @pytest.mark.parametrize("n_q,n_kv,h,hk", [(1, 20000, 2, 1), (3, 5000, 1, 1), (130, 9000, 4, 1)])
 def test_key_splits_join(cuda_device, dtype, d, n_q, n_kv, h, hk):
