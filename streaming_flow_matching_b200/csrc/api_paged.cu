@@ -35,7 +35,8 @@ int fill_cache(PagedCache* c, const void* k_pages, const void* v_pages, const in
   // rows and slots are 32-bit numbers in the kernels, byte offsets 64-bit ones
   if ((long long)n_pages * page_size > INT_MAX || (long long)max_pages * page_size > INT_MAX / 2)
     return SFM_EUNSUPPORTED;
-  if ((long long)n_seq * ((long long)max_pages * page_size + 64) / 64 > INT_MAX) return SFM_EUNSUPPORTED;
+  if ((long long)n_seq * ((long long)max_pages * page_size + 64) / 64 > INT_MAX / 2)
+    return SFM_EUNSUPPORTED;
   c->table = table;
   c->lengths = lengths;
   c->n_seq = n_seq;
@@ -76,7 +77,7 @@ int sfm_paged_append(const void* k, const void* v, void* k_pages, void* v_pages,
                   head_dim, state ? cap : -1);
   if (rc) return rc;
   const long long row_bytes = (long long)n_kv_heads * head_dim * elem_bytes(dtype);
-  if (row_bytes > (1 << 24)) return SFM_EUNSUPPORTED;
+  if (row_bytes > (1 << 24) || n_rows > INT_MAX - 256) return SFM_EUNSUPPORTED;
   Guard gd;
   if ((rc = call_guard(&gd))) return rc;
   a.k = k;
@@ -96,6 +97,7 @@ int sfm_paged_append(const void* k, const void* v, void* k_pages, void* v_pages,
 size_t sfm_paged_attention_workspace_bytes(int n_seq, int max_tokens, int n_heads, int n_kv_heads, int head_dim,
                                            int dtype, int with_weights) {
   if (n_seq < 1 || max_tokens < 1 || check_heads(n_heads, n_kv_heads, head_dim, dtype)) return 0;
+  if (!fits_grid((long long)n_seq * n_heads)) return 0;
   return paged_attention_workspace(n_seq, max_tokens, n_heads, n_kv_heads, head_dim, dtype, with_weights != 0);
 }
 
@@ -178,6 +180,7 @@ int sfm_paged_evict(void* k_pages, void* v_pages, const int* table, const int* l
 int sfm_attention_bounds(int n_q, int n_kv, const int* doc_starts, const int* prefixes, int n_docs, int causal,
                          int* key_lo, int* key_hi, void* stream) {
   if (n_q < 1 || n_kv < n_q || !key_lo || !key_hi || (causal != 0 && causal != 1)) return SFM_EINVAL;
+  if (n_kv > INT_MAX - 256) return SFM_EUNSUPPORTED;
   if (n_docs < 0 || (doc_starts && n_docs < 1) || (!doc_starts && n_docs != (prefixes ? 1 : 0))) return SFM_EINVAL;
   if (!aligned(doc_starts, 4) || !aligned(prefixes, 4) || !aligned(key_lo, 4) || !aligned(key_hi, 4))
     return SFM_EINVAL;
@@ -188,6 +191,7 @@ int sfm_attention_bounds(int n_q, int n_kv, const int* doc_starts, const int* pr
 size_t sfm_attention_masked_workspace_bytes(int n_q, int n_kv, int n_heads, int n_kv_heads, int head_dim,
                                             int dtype) {
   if (n_q < 1 || n_kv < 1 || check_heads(n_heads, n_kv_heads, head_dim, dtype)) return 0;
+  if (n_q > INT_MAX - 256 || n_kv > INT_MAX - 256) return 0;
   return masked_workspace(n_q, n_kv, n_heads, n_kv_heads, head_dim, dtype);
 }
 

@@ -104,6 +104,20 @@ def test_bounds_arguments(bad):
     assert L.lib.sfm_attention_bounds(*a.values(), None) == L.SFM_EINVAL
 
 
+def test_sizes_past_what_32_bits_index():
+    top = 2 ** 31 - 1
+    assert append(n_rows=top) == L.SFM_EUNSUPPORTED
+    assert L.lib.sfm_attention_bounds(top, top, P, P, 2, 1, P, P, None) == L.SFM_EUNSUPPORTED
+    assert masked(n_q=4, n_kv=top) == L.SFM_EUNSUPPORTED
+    assert L.lib.sfm_attention_masked_workspace_bytes(top, top, 4, 2, 128, BF) == 0
+    assert L.lib.sfm_attention_masked_workspace_bytes(4, top, 4, 2, 32, F32) == 0
+    assert L.lib.sfm_paged_attention_workspace_bytes(top, 100, 4, 2, 128, BF, 0) == 0
+    assert attention(n_seq=top // 2, h=4) == L.SFM_EUNSUPPORTED
+    # tiles of all sequences together, were every one as long as its table
+    assert attention(n_seq=1 << 11, width=1 << 25, page=32, n_pages=1, weights=None, positions=None,
+                     q_positions=None) == L.SFM_EUNSUPPORTED
+
+
 def test_workspaces():
     att = L.lib.sfm_paged_attention_workspace_bytes
     assert att(4, 1000, 24, 8, 128, BF, 0) % 16 == 0
