@@ -28,7 +28,12 @@
 // Few query rows over many keys: the key tiles are cut into splits whose fp32 partials a
 // second kernel joins.
 //
-// fp32 runs on the CUDA cores in 32 x 64 tiles.
+// Measured (bf16): a block's 256 rows over 128 keys take ~1.9 us in the steady state, 1.3
+// PFLOP/s, the softmax as long as the products beside it; set-up and output of a block 6 to 9
+// us.  8,192 packed causal queries of 24 heads, cap 50: 194 us (172 without the cap); 8,000 with
+// prefixes and a bias: 418 us (393 without); 48 queries over 2,148 keys: 17 us.
+//
+// fp32 runs on the CUDA cores in 32 x 64 tiles: 1,000 queries of 4 heads 29 us.
 #include <limits.h>
 #include <math.h>
 
@@ -901,9 +906,9 @@ constexpr int f32_smem() {
   return ((FM + 2 * FN) * (32 * DV + 4) + FM * (FN + 4)) * 4;
 }
 
-// 32 query rows x 64 keys per step (64 rows left half the SMs without work at 1,000 queries of
-// four heads: 68 us, now 29 us with key splits); thread (ty, tx) of 8 x 16 holds 4 rows x 4 scores
-// (keys tx + 16 k) and 4 rows x 2 DV outputs.  Masked scores are skipped by weight 0 and
+// 32 query rows x 64 keys per step and key splits (64 rows without splits left half the SMs
+// without work at 1,000 queries of four heads: 68 us instead of 29); thread (ty, tx) of 8 x 16
+// holds 4 rows x 4 scores (keys tx + 16 k) and 4 rows x 2 DV outputs.  Masked scores are skipped by weight 0 and
 // masked V rows by staging zeros for keys that no row of the tile sees; a key that only
 // some rows see and that holds a non-finite value is left out row by row.
 // n_splits > 1: the tiles of the rows' union are cut into that many runs, each writing a

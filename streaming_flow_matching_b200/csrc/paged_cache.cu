@@ -15,7 +15,12 @@
 //   select  one CTA per (sequence, key head): the keep-th largest rank by radix
 //           selection (digits of 11, 11 and 10 bits, a histogram each), then the
 //           lists of evicted slots < keep and kept slots >= keep in slot order
-//   move    a warp per moved row (K and V rows of one head, weight, position)
+//   move    a warp per 8 moved rows (K and V rows of one head, weight, position)
+//
+// Measured (bf16): append of 8 x ~1,150 rows of 24 heads 38.7 us, 5.9 TB/s (0.89 of a copy's
+// rate).  Eviction of 16 sequences x 8 heads from 30,500-36,000 to 30,000 slots 110 us: select 31 us,
+// bound by its instructions (62 % issue); moves 70 us, bound by memory at 256 bytes a piece;
+// of 4 x 1,200 to 924: 14 us, latency.
 #include <limits.h>
 
 #include "paged.cuh"
