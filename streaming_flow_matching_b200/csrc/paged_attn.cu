@@ -27,7 +27,7 @@
 // a copy's rate; 16 sequences of 500 to 12,000 tokens, 8 key heads of 3 query heads: 60 us,
 // 5.7 TB/s, 62 us with a cap, 73 us with the cap and weights (the pass that adds them waits for
 // its scores to come from L2, and for the sums).  2 sequences of 300 tokens: 7.6 us, the latency
-// of two kernels.  fp32, 8 sequences of up to 4,000, 2 key heads: 21 us.
+// of two kernels.  fp32, 8 sequences of 900 to 4,000, 2 key heads of 4, D 64: 11.4 us.
 #include <math.h>
 
 #include "paged.cuh"
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t vs_base = ks_base + kWarpTok * 256;
     const int tok = cw.tile * kTile + warp * kWarpTok + g;    // this thread's tokens: tok, tok + 8
     const unsigned mk = masks[0];
-    if (mk) {
+    if (mk || sp.scores) {                                    // (-inf is a score: bad pages)
       float s[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -399,13 +399,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
-    } else if (sp.scores) {
-      // past the sequence's end, or all on bad pages: the pass after this reads the latter
-      for (int x = lane; x < nh * kWarpTok; x += 32) {
-        const int t = cw.tile * kTile + warp * kWarpTok + (x & (kWarpTok - 1));
-        if (t < cw.len)
-          sp.scores[((size_t)cw.seq * a.heads + h0 + x / kWarpTok) * sp.pitch + t] = -INFINITY;
-      }
     }
     __syncwarp();                                             // the stage may be refilled
 #pragma unroll
@@ -474,17 +467,39 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ------------------------------------------------------------------ fp32, D = 32 DV
 
-// CUDA cores.  A warp takes 4 tokens at a time, 8 lanes to a token: lane j of the eight
-// holds the 16-byte pieces j + 8 i of the row, so a load instruction covers whole
-// 128-byte lines, and a score takes three shuffles for four tokens.  GT query heads per
-// CTA (a larger group reads its keys again, from L2).
+// CUDA cores.  A warp takes 16 tokens (8 for D = 128) at a time, in steps of 4, 8 lanes to a
+// token: lane j of the eight holds the 16-byte pieces j + 8 i of the row, so a load covers whole
+// 128-byte lines.  Rows come through a ring of cp.async stages, in which each lane finds the
+// pieces that it fetched itself (no exchange, no bank conflicts).  The 8 lanes' sums of all
+// (head, step) scores are reduced and scattered in one go: with 4 heads and 4 steps 14 shuffles
+// leave each lane two scores, whose cap, bias and exponential are then done once and not by 8
+// lanes (with the deeper ring: 21 -> 11.4 us at the size above).  GT query heads per CTA (a larger group reads its keys again, from
+// L2).
+template <int DV>
+struct F32Ring {
+  static constexpr int kSteps = DV == 4 ? 2 : 4, kTok = 4 * kSteps, kSub = kWarpTok / kTok;
+  static constexpr int kHalf = kTok * DV * 128;                // bytes of a stage's K (or V)
+  static constexpr int kDepth = DV == 3 ? 2 : 3;               // 24 KB a warp (DV = 1: 12)
+  static constexpr int kBytes = kDepth * 2 * kHalf;
+};
 template <int DV, int GT>
-__global__ void __launch_bounds__(kThreads)
+constexpr int f32_smem() {                                     // rings, Q, O and (max, sum) of each warp
+  return kWarps * F32Ring<DV>::kBytes + GT * DV * 128 + kWarps * GT * (DV * 128 + 8);
+}
+
+template <int DV, int GT>
+__global__ void __launch_bounds__(kThreads, 2)
     paged_attn_fp32_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp) {
-  constexpr int D = 32 * DV;
-  __shared__ float4 qs[GT][D / 4];
-  __shared__ float obuf[kWarps][GT][D];
-  __shared__ float mlbuf[kWarps][GT][2];
+  using Ring = F32Ring<DV>;
+  constexpr int D = 32 * DV, STEPS = Ring::kSteps, TOK = Ring::kTok, DEPTH = Ring::kDepth;
+  constexpr int NV = GT * STEPS;                               // scores of a step group, v = head * STEPS + step
+  constexpr int NO = NV >= 8 ? NV / 8 : 1;                     // of them a lane's own: v0, ... of one head,
+  constexpr int DUP = NV >= 8 ? 1 : 8 / NV;                    // held by that many lanes
+  constexpr int LPH = 8 / GT;                                  // lanes (of 8) of a head
+  extern __shared__ __align__(16) uint8_t smem[];
+  float4* qs = reinterpret_cast<float4*>(smem + kWarps * Ring::kBytes);    // [GT][D / 4]
+  float* obuf = reinterpret_cast<float*>(qs + GT * (D / 4));               // [kWarps][GT][D]
+  float* mlbuf = obuf + kWarps * GT * D;                                   // [kWarps][GT][2]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int j = lane & 7, grp = lane >> 3;
   const int hg = blockIdx.x % sp.hgroups, slot = blockIdx.x / sp.hgroups;
@@ -499,12 +514,14 @@ __global__ void __launch_bounds__(kThreads)
   const int chunk = (total + sp.slots - 1) / sp.slots;
   const int b0 = slot * chunk, b1 = min(total, b0 + chunk);
   if (b0 >= b1) return;
-  Walk cw;
-  find_tile(a.c, b0, lane, &cw.seq, &cw.tile);
-  cw.len = cache_len(a.c, cw.seq, nullptr);
+  Walk ld;                                                    // of the loads
+  find_tile(a.c, b0, lane, &ld.seq, &ld.tile);
+  ld.len = cache_len(a.c, ld.seq, nullptr);
+  Walk cw = ld;                                               // of the arithmetic
   const size_t row_vecs = (size_t)a.c.kv_heads * (D / 4);
-  const float4* kp = reinterpret_cast<const float4*>(a.k_pages) + (size_t)hk * (D / 4);
-  const float4* vp = reinterpret_cast<const float4*>(a.v_pages) + (size_t)hk * (D / 4);
+  const float4* kp = reinterpret_cast<const float4*>(a.k_pages) + (size_t)hk * (D / 4) + j;
+  const float4* vp = reinterpret_cast<const float4*>(a.v_pages) + (size_t)hk * (D / 4) + j;
+  uint8_t* ring = smem + warp * Ring::kBytes + lane * 16;     // this lane's pieces
   const float scale = rsqrtf((float)D);
   const bool cap = a.softcap > 0.f;
   const float inv_cap = cap ? 1.f / a.softcap : 0.f;
@@ -514,26 +531,49 @@ __global__ void __launch_bounds__(kThreads)
     const int t = w.tile * kTile + warp * kWarpTok + lane;
     return lane < kWarpTok && t < w.len ? cache_row(a.c, w.seq, t, a.err) : -1;
   };
-  float4 kn[DV], vn[DV];
-  auto load_rows = [&](int row) {
+  const int n_its = (b1 - b0) * Ring::kSub;
+  unsigned masks[DEPTH] = {};                                 // which of a stage's tokens count
+  int pos[DEPTH][NO];                                         // and the positions of the lane's own
+  const int v0 = j * NV / 8, my_head = v0 / STEPS, my_step = v0 % STEPS;
+  int next_row = lookup(ld), to_issue = 0;
+  auto issue = [&](unsigned* mask, int* at) {
+    const int sub = to_issue % Ring::kSub;
 #pragma unroll
-    for (int i = 0; i < DV; ++i) {
-      kn[i] = vn[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (row >= 0) {
-        kn[i] = __ldg(kp + (size_t)row * row_vecs + j + 8 * i);
-        vn[i] = __ldg(vp + (size_t)row * row_vecs + j + 8 * i);
+    for (int e = 0; e < NO; ++e) {
+      at[e] = ld.tile * kTile + warp * kWarpTok + sub * TOK + (my_step + e) * 4 + grp;
+      if (a.positions && at[e] < ld.len)
+        at[e] = __ldg(a.positions + ((size_t)ld.seq * a.c.kv_heads + hk) * a.cap + at[e]);
+    }
+    const uint32_t dst = smem_u32(ring) + (uint32_t)(to_issue % DEPTH) * (2 * Ring::kHalf);
+    *mask = (__ballot_sync(0xffffffffu, next_row >= 0) >> (sub * TOK)) & ((1u << TOK) - 1u);
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) {
+      const int row = __shfl_sync(0xffffffffu, next_row, sub * TOK + st * 4 + grp);
+      const size_t off = (size_t)max(row, 0) * row_vecs;
+#pragma unroll
+      for (int i = 0; i < DV; ++i) {
+        const uint32_t d = dst + (uint32_t)((st * DV + i) * 512);
+        cp_async16(d, kp + off + 8 * i, row >= 0);
+        cp_async16(d + Ring::kHalf, vp + off + 8 * i, row >= 0);
       }
     }
+    ++to_issue;
+    if (to_issue % Ring::kSub == 0 && to_issue < n_its) {
+      ld.next(a.c);
+      next_row = lookup(ld);
+    }
   };
-  int row16 = lookup(cw);
-  int row_now = __shfl_sync(0xffffffffu, row16, grp);
-  load_rows(row_now);
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) {
+    if (to_issue < n_its) issue(&masks[i], pos[i]);
+    cp_commit();
+  }
 
   float4 acc[GT][DV];
-  float m[GT], l[GT], slope[GT];
+  float m = -INFINITY, l = 0.f, slope = 0.f;                  // of my_head
   bool fresh = true, seg_start = false;
   int q_pos = 0;
-  for (int b = b0; b < b1; ++b) {
+  for (int it = 0; it < n_its; ++it) {
     if (fresh) {
       fresh = false;
       seg_start = cw.tile != 0;
@@ -541,131 +581,169 @@ __global__ void __launch_bounds__(kThreads)
         const int hh = x / (D / 4), c = x - hh * (D / 4);
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
         if (hh < nh) f = __ldg(reinterpret_cast<const float4*>(a.q) + ((size_t)cw.seq * a.heads + h0 + hh) * (D / 4) + c);
-        qs[hh][c] = f;
+        qs[x] = f;
       }
+      m = -INFINITY;
+      l = 0.f;
+      slope = a.slopes && my_head < nh ? __ldg(a.slopes + h0 + my_head) : 0.f;
 #pragma unroll
-      for (int hh = 0; hh < GT; ++hh) {
-        m[hh] = -INFINITY;
-        l[hh] = 0.f;
-        slope[hh] = a.slopes && hh < nh ? __ldg(a.slopes + h0 + hh) : 0.f;
+      for (int hh = 0; hh < GT; ++hh)
 #pragma unroll
         for (int i = 0; i < DV; ++i) acc[hh][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
       q_pos = a.q_positions ? __ldg(a.q_positions + cw.seq) : cw.len - 1;
       __syncthreads();
     }
-    const int base = cw.tile * kTile + warp * kWarpTok;
-    Walk nw = cw;
-    if (b + 1 < b1) nw.next(a.c);
-    const int next16 = b + 1 < b1 ? lookup(nw) : -1;
+    const int sub = it % Ring::kSub;
+    const int base = cw.tile * kTile + warp * kWarpTok + sub * TOK;
+    if (to_issue < n_its) issue(&masks[DEPTH - 1], pos[DEPTH - 1]);
+    cp_commit();
+    cp_wait<DEPTH - 1>();
+    const unsigned mk = masks[0];
+    if (mk || sp.scores) {                                     // (-inf is a score: bad pages)
+      const float4* kst = reinterpret_cast<const float4*>(ring + (it % DEPTH) * (2 * Ring::kHalf));
+      const float4* vst = kst + Ring::kHalf / 16;
+      float s[NV];
 #pragma unroll
-    for (int step = 0; step < kWarpTok / 4; ++step) {
-      const int tok = base + step * 4 + grp;
-      // the rows of the step after this one are on their way while this one is computed
-      const int row = row_now;
-      float4 kf[DV], vf[DV];
+      for (int v = 0; v < NV; ++v) s[v] = 0.f;
 #pragma unroll
       for (int i = 0; i < DV; ++i) {
-        kf[i] = kn[i];
-        vf[i] = vn[i];
-      }
-      row_now = step + 1 < kWarpTok / 4 ? __shfl_sync(0xffffffffu, row16, (step + 1) * 4 + grp)
-                                        : __shfl_sync(0xffffffffu, next16, grp);
-      load_rows(row_now);
-      float dist = 0.f;
-      if (a.slopes && row >= 0) {
-        const int p = a.positions ? __ldg(a.positions + ((size_t)cw.seq * a.c.kv_heads + hk) * a.cap + tok) : tok;
-        dist = fabsf((float)((long long)q_pos - p));
-      }
+        float4 kf[STEPS];
 #pragma unroll
-      for (int hh = 0; hh < GT; ++hh) {
-        float s = 0.f;
+        for (int st = 0; st < STEPS; ++st) kf[st] = kst[(st * DV + i) * 32];
 #pragma unroll
-        for (int i = 0; i < DV; ++i) {
-          const float4 qv = qs[hh][j + 8 * i];
-          s = fmaf(qv.x, kf[i].x, s);
-          s = fmaf(qv.y, kf[i].y, s);
-          s = fmaf(qv.z, kf[i].z, s);
-          s = fmaf(qv.w, kf[i].w, s);
-        }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        s += __shfl_xor_sync(0xffffffffu, s, 4);
-        if (row < 0) s = -INFINITY;
-        else if (cap) s = finish_score<true>(s, scale, a.softcap, inv_cap, slope[hh], dist);
-        else s = finish_score<false>(s, scale, 0.f, 0.f, slope[hh], dist);
-        if (sp.scores && j == 0 && hh < nh && tok < cw.len)
-          sp.scores[((size_t)cw.seq * a.heads + h0 + hh) * sp.pitch + tok] = s;
-        if (__any_sync(0xffffffffu, s > m[hh] + kGrow)) {      // each group of 8 lanes has its own max
-          const float mx = fmaxf(m[hh], s);
-          const float al = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - mx);
-          m[hh] = mx;
-          l[hh] *= al;
+        for (int hh = 0; hh < GT; ++hh) {
+          const float4 qv = qs[hh * (D / 4) + j + 8 * i];
 #pragma unroll
-          for (int i = 0; i < DV; ++i) {
-            acc[hh][i].x *= al;
-            acc[hh][i].y *= al;
-            acc[hh][i].z *= al;
-            acc[hh][i].w *= al;
+          for (int st = 0; st < STEPS; ++st) {
+            float x = s[hh * STEPS + st];
+            x = fmaf(qv.x, kf[st].x, x);
+            x = fmaf(qv.y, kf[st].y, x);
+            x = fmaf(qv.z, kf[st].z, x);
+            s[hh * STEPS + st] = fmaf(qv.w, kf[st].w, x);
           }
         }
-        const float p = ex2_approx(s - (m[hh] == -INFINITY ? 0.f : m[hh]));
-        l[hh] += p;
+      }
+      // the sums over the 8 lanes; lane j ends with those of v0 = j NV / 8 (+ 1)
 #pragma unroll
-        for (int i = 0; i < DV; ++i) {
-          acc[hh][i].x = fmaf(p, vf[i].x, acc[hh][i].x);
-          acc[hh][i].y = fmaf(p, vf[i].y, acc[hh][i].y);
-          acc[hh][i].z = fmaf(p, vf[i].z, acc[hh][i].z);
-          acc[hh][i].w = fmaf(p, vf[i].w, acc[hh][i].w);
+      for (int b = 0; b < 3; ++b) {
+        const int o = 4 >> b, n = NV >> (b + 1);
+        const bool up = (j & o) != 0;
+        if (n == 0) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const float got = __shfl_xor_sync(0xffffffffu, up ? s[i] : s[i + n], o);
+          s[i] = (up ? s[i + n] : s[i]) + got;
+        }
+      }
+      bool grow = false;
+#pragma unroll
+      for (int e = 0; e < NO; ++e) {
+        const int x = (my_step + e) * 4 + grp;                 // token of the stage
+        const float dist = fabsf((float)((long long)q_pos - pos[0][e]));
+        if (!((mk >> x) & 1u)) s[e] = -INFINITY;
+        else if (cap) s[e] = finish_score<true>(s[e], scale, a.softcap, inv_cap, slope, dist);
+        else s[e] = finish_score<false>(s[e], scale, 0.f, 0.f, slope, dist);
+        grow |= s[e] > m + kGrow;                              // also from m = -inf
+        if (sp.scores && my_head < nh && base + x < cw.len)
+          sp.scores[((size_t)cw.seq * a.heads + h0 + my_head) * sp.pitch + base + x] = s[e];
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        float mx = m;
+#pragma unroll
+        for (int e = 0; e < NO; ++e) mx = fmaxf(mx, s[e]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+          if (o < LPH || o >= 8) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float al = m == -INFINITY ? 0.f : ex2_approx(m - mx);
+        m = mx;
+        l *= al;
+#pragma unroll
+        for (int hh = 0; hh < GT; ++hh) {
+          const float f = __shfl_sync(0xffffffffu, al, hh * LPH);
+#pragma unroll
+          for (int i = 0; i < DV; ++i) {
+            acc[hh][i].x *= f;
+            acc[hh][i].y *= f;
+            acc[hh][i].z *= f;
+            acc[hh][i].w *= f;
+          }
+        }
+      }
+      const float mb = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int e = 0; e < NO; ++e) {
+        s[e] = ex2_approx(s[e] - mb);
+        l += s[e];
+      }
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        float4 vf[DV];
+#pragma unroll
+        for (int i = 0; i < DV; ++i) vf[i] = vst[(st * DV + i) * 32];
+#pragma unroll
+        for (int hh = 0; hh < GT; ++hh) {
+          const int v = hh * STEPS + st;
+          const float p = __shfl_sync(0xffffffffu, s[v % NO], grp * 8 + v * 8 / NV);
+#pragma unroll
+          for (int i = 0; i < DV; ++i) {
+            acc[hh][i].x = fmaf(p, vf[i].x, acc[hh][i].x);
+            acc[hh][i].y = fmaf(p, vf[i].y, acc[hh][i].y);
+            acc[hh][i].z = fmaf(p, vf[i].z, acc[hh][i].z);
+            acc[hh][i].w = fmaf(p, vf[i].w, acc[hh][i].w);
+          }
         }
       }
     }
-    row16 = next16;
+    __syncwarp();                                              // the stage may be refilled
+#pragma unroll
+    for (int i = 0; i + 1 < DEPTH; ++i) {
+      masks[i] = masks[i + 1];
+#pragma unroll
+      for (int e = 0; e < NO; ++e) pos[i][e] = pos[i + 1][e];
+    }
+    if (sub + 1 < Ring::kSub) continue;
     const int seq = cw.seq;
     const bool seq_done = (cw.tile + 1) * kTile >= cw.len;
-    cw = nw;
-    if (!seq_done && b + 1 < b1) continue;
+    if (it + 1 < n_its) cw.next(a.c);
+    if (!seq_done && it + 1 < n_its) continue;
 
+    // ---- the sequence, or the run, ends here: the warp's four groups, then the four warps
     fresh = true;
     Segment sg{seg_start, !seq_done};
+    float sum = l * (1.f / DUP);
 #pragma unroll
-    for (int hh = 0; hh < GT; ++hh) {
-      // the warp's four groups, then its result to shared memory
-      float mw = m[hh];
-      mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 8));
-      mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 16));
-      const float f = m[hh] == -INFINITY ? 0.f : ex2_approx(m[hh] - mw);
-      float lw = l[hh] * f;
-      lw += __shfl_xor_sync(0xffffffffu, lw, 8);
-      lw += __shfl_xor_sync(0xffffffffu, lw, 16);
+    for (int o = 1; o < 32; o <<= 1)
+      if (o < LPH || o >= 8) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (grp == 0 && j % LPH == 0) {
+      mlbuf[(warp * GT + my_head) * 2] = m;
+      mlbuf[(warp * GT + my_head) * 2 + 1] = sum;
+    }
+#pragma unroll
+    for (int hh = 0; hh < GT; ++hh)
 #pragma unroll
       for (int i = 0; i < DV; ++i) {
-        float v[4] = {acc[hh][i].x * f, acc[hh][i].y * f, acc[hh][i].z * f, acc[hh][i].w * f};
+        float v[4] = {acc[hh][i].x, acc[hh][i].y, acc[hh][i].z, acc[hh][i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[e] += __shfl_xor_sync(0xffffffffu, v[e], 8);
           v[e] += __shfl_xor_sync(0xffffffffu, v[e], 16);
         }
-        if (grp == 0) *reinterpret_cast<float4*>(&obuf[warp][hh][(j + 8 * i) * 4]) = make_float4(v[0], v[1], v[2], v[3]);
+        if (grp == 0)
+          *reinterpret_cast<float4*>(obuf + (warp * GT + hh) * D + (j + 8 * i) * 4) = make_float4(v[0], v[1], v[2], v[3]);
       }
-      if (lane == 0) {
-        mlbuf[warp][hh][0] = mw;
-        mlbuf[warp][hh][1] = lw;
-      }
-    }
     __syncthreads();
     for (int x = threadIdx.x; x < nh * D; x += kThreads) {
       const int hh = x / D, d = x - hh * D;
       float mm = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mlbuf[w][hh][0]);
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mlbuf[(w * GT + hh) * 2]);
       const float mb = mm == -INFINITY ? 0.f : mm;
       float sum = 0.f, o = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2_approx(mlbuf[w][hh][0] - mb);
-        sum = fmaf(f, mlbuf[w][hh][1], sum);
-        o = fmaf(f, obuf[w][hh][d], o);
+        const float f = ex2_approx(mlbuf[(w * GT + hh) * 2] - mb);
+        sum = fmaf(f, mlbuf[(w * GT + hh) * 2 + 1], sum);
+        o = fmaf(f, obuf[(w * GT + hh) * D + d], o);
       }
       if (sg.partial()) {
         const size_t at = (((size_t)slot * sp.hgroups + hg) * 2 + sg.index()) * sp.hpt + hh;
@@ -682,6 +760,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
   }
+  cp_wait<0>();
 }
 
 // ------------------------------------------------------------------ join
@@ -872,8 +951,7 @@ Plan make_plan(int n_seq, int max_tokens, int heads, int kv_heads, int head_dim,
   sp.hpt = heads_per_tile(G, dtype);
   sp.gt = (G + sp.hpt - 1) / sp.hpt;
   sp.hgroups = kv_heads * sp.gt;
-  // one wave: two CTAs per SM (bf16, by shared memory), four (fp32, by registers)
-  const int ctas = kSms * (dtype == SFM_DTYPE_BF16 ? 2 : 4);
+  const int ctas = kSms * 2;                                   // one wave: two per SM, by shared memory
   sp.slots = ctas / sp.hgroups < 1 ? 1 : ctas / sp.hgroups;
   char* at = (char*)ws;
   auto take = [&](size_t floats) {
@@ -905,11 +983,19 @@ cudaError_t launch_bf16(const DecodeArgs& a, const Split& sp, unsigned grid, cud
   return launch_dependent(kernel, grid, kThreads, kSmemBf16, s, a, sp);
 }
 
+template <int DV, int GT>
+cudaError_t launch_fp32(const DecodeArgs& a, const Split& sp, unsigned grid, cudaStream_t s) {
+  constexpr int smem = f32_smem<DV, GT>();
+  const cudaError_t e =
+      cudaFuncSetAttribute(paged_attn_fp32_kernel<DV, GT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_attn_fp32_kernel<DV, GT>, grid, kThreads, smem, s, a, sp);
+}
 template <int DV>
 cudaError_t launch_fp32(const DecodeArgs& a, const Split& sp, unsigned grid, cudaStream_t s) {
-  if (sp.hpt == 4) return launch_dependent(paged_attn_fp32_kernel<DV, 4>, grid, kThreads, 0, s, a, sp);
-  if (sp.hpt == 2) return launch_dependent(paged_attn_fp32_kernel<DV, 2>, grid, kThreads, 0, s, a, sp);
-  return launch_dependent(paged_attn_fp32_kernel<DV, 1>, grid, kThreads, 0, s, a, sp);
+  if (sp.hpt == 4) return launch_fp32<DV, 4>(a, sp, grid, s);
+  if (sp.hpt == 2) return launch_fp32<DV, 2>(a, sp, grid, s);
+  return launch_fp32<DV, 1>(a, sp, grid, s);
 }
 
 }  // namespace
