@@ -208,7 +208,7 @@ int sfm_attention_masked(const void* q, const void* k, const void* v, void* o, i
       !aligned(key_hi, 4) || !aligned(slopes, 4))
     return SFM_EINVAL;
   if (n_q > INT_MAX - 256 || n_kv > INT_MAX - 256 || !fits_grid((long long)n_q * n_heads) ||
-      !fits_grid(((long long)n_q / 32 + 1) * n_heads * 16)) return SFM_EUNSUPPORTED;
+      !fits_grid(((long long)n_q / 32 + 1) * n_heads * 32)) return SFM_EUNSUPPORTED;
   const size_t need = masked_workspace(n_q, n_kv, n_heads, n_kv_heads, head_dim, dtype);
   if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 16)))) return SFM_EINVAL;
   MaskedArgs a{q, k, v, o, n_q, n_kv, n_heads, n_kv_heads, head_dim, key_lo, key_hi, softcap, slopes};

@@ -33,7 +33,8 @@
 // us.  8,192 packed causal queries of 24 heads, cap 50: 194 us (172 without the cap); 8,000 with
 // prefixes and a bias: 418 us (393 without); 48 queries over 2,148 keys: 17 us.
 //
-// fp32 runs on the CUDA cores in 32 x 64 tiles: 1,000 queries of 4 heads 29 us.
+// fp32 runs on the CUDA cores in 32 x 64 tiles: 1,000 queries over 1,400 keys, 4 heads, D 64, in
+// documents 26 us; 1,000 over 6,000, 24 heads 1.29 ms, 28.6 TFLOP/s.
 #include <limits.h>
 #include <math.h>
 
@@ -101,7 +102,7 @@ constexpr int OFF_BAR = OFF_V + VST * TILE;
 constexpr int SMEM = OFF_BAR + 512 + 1024;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kMaxKeySplits = 16;
+constexpr int kMaxKeySplits = 32;                               // a lane each in the join
 constexpr int kSms = 148;
 
 struct TcArgs {
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(256)
   const long long gw = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (gw >= rows_heads) return;
-  // lane s holds split s's log-sum-exp (at most 16 splits)
+  // lane s holds split s's log-sum-exp (at most 32 splits)
   const float mine = lane < n_splits ? lse_part[lane * rows_heads + gw] : -INFINITY;
   float mx = mine;
 #pragma unroll
@@ -901,14 +902,44 @@ int launch_join(const float* o_part, const float* lse_part, void* o, long long r
 
 constexpr int FM = 32, FN = 64, FTHREADS = 128;
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
+}
+// tanh to about 4e-7 of its value without a branch: as tanh_ex2, the series up to x^9 (the next
+// term is 1382 x^11 / 155925, 6e-8 of x at 0.3)
+__device__ __forceinline__ float tanh_f32(float x) {
+  const float y = x * x;
+  float p = fmaf(y, 62.f / 2835.f, -17.f / 315.f);
+  p = fmaf(p, y, 2.f / 15.f);
+  p = fmaf(p, y, -1.f / 3.f);
+  const float big = 1.f - __fdividef(2.f, ex2_approx(x * (2.f * kLog2e)) + 1.f);
+  return fabsf(x) < 0.3f ? fmaf(x * y, p, x) : big;
+}
+
+__device__ __forceinline__ void ld_pairs(const void* src, F2 (&d)[2]) {      // 16 bytes of shared memory
+  const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(src);
+  d[0].v = x.x;
+  d[1].v = x.y;
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int DV>
 constexpr int f32_smem() {
   return ((FM + 2 * FN) * (32 * DV + 4) + FM * (FN + 4)) * 4;
 }
 
 // 32 query rows x 64 keys per step and key splits (64 rows without splits left half the SMs
-// without work at 1,000 queries of four heads: 68 us instead of 29); thread (ty, tx) of 8 x 16
-// holds 4 rows x 4 scores (keys tx + 16 k) and 4 rows x 2 DV outputs.  Masked scores are skipped by weight 0 and
+// without work at 1,000 queries of four heads: 68 us); thread (ty, tx) of 8 x 16 holds 4 rows x
+// 4 scores (keys tx + 16 k) and 4 rows x 2 DV outputs, as pairs of fp32 (even and odd dims of a
+// score; neighbouring dims of an output).  K and V come by asynchronous copies, each while the
+// other is at work; a tile alone on its SM takes 3.4 us (5 with loads in pairs through registers),
+// bound then by latency, and among others by shared memory: a product of 2 x 2 fp32 per 16 bytes
+// read is half of what the FMA pipes could take.  Masked scores are skipped by weight 0 and
 // masked V rows by staging zeros for keys that no row of the tile sees; a key that only
 // some rows see and that holds a non-finite value is left out row by row.
 // n_splits > 1: the tiles of the rows' union are cut into that many runs, each writing a
@@ -971,103 +1002,119 @@ __global__ void __launch_bounds__(FTHREADS)
   const float inv_cap = cap ? 1.f / a.softcap : 0.f;
   const float slope = a.slopes ? __ldg(a.slopes + h) : 0.f;
   float m[4], l[4];
-  float o[4][2 * DV];
+  F2 o[4][DV];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2 * DV; ++e) o[i][e] = 0.f;
+    for (int e = 0; e < DV; ++e) o[i][e] = F2(0.f, 0.f);
   }
   const int tile0 = u_lo < u_hi ? u_lo / FN : 0, tiles = u_lo < u_hi ? (u_hi + FN - 1) / FN - tile0 : 0;
   const int run = (tiles + n_splits - 1) / n_splits;
-  const int k_end = (tile0 + min(tiles, (split + 1) * run)) * FN;
-  for (int k0 = (tile0 + min(tiles, split * run)) * FN; k0 < k_end; k0 += FN) {
-    __syncthreads();
-    bool odd = false;                                          // a non-finite V element here
-    for (int x = tid; x < FN * (DD / 4); x += FTHREADS) {
-      const int rr = x / (DD / 4), c = x - rr * (DD / 4);
-      float4 fk = make_float4(0.f, 0.f, 0.f, 0.f), fv = fk;
-      if (k0 + rr >= u_lo && k0 + rr < u_hi) {
-        fk = __ldg(reinterpret_cast<const float4*>(k + (size_t)(k0 + rr) * ldk + 4 * c));
-        fv = __ldg(reinterpret_cast<const float4*>(v + (size_t)(k0 + rr) * ldk + 4 * c));
-        odd |= !(isfinite(fv.x) && isfinite(fv.y) && isfinite(fv.z) && isfinite(fv.w));
+  const int k_begin = (tile0 + min(tiles, split * run)) * FN, k_end = (tile0 + min(tiles, (split + 1) * run)) * FN;
+  // a tile of K or V on its way to shared memory, zeros for keys that no row sees
+  auto fetch = [&](float* dst, const float* src, int k0) {
+    if (k0 < k_end) {
+#pragma unroll 4
+      for (int x = tid; x < FN * (DD / 4); x += FTHREADS) {
+        const int rr = x / (DD / 4), c = x - rr * (DD / 4);
+        const bool in = k0 + rr >= u_lo && k0 + rr < u_hi;
+        cp_async16(smem_u32(dst + rr * P + 4 * c), src + (size_t)(in ? k0 + rr : u_lo) * ldk + 4 * c, in);
       }
-      *reinterpret_cast<float4*>(ks + rr * P + 4 * c) = fk;
-      *reinterpret_cast<float4*>(vs + rr * P + 4 * c) = fv;
     }
-    odd = __syncthreads_or(odd);
-    float s[4][4];
+    cp_commit();
+  };
+  // K of the next tile comes while this one's softmax and V are at work, V during the next scores
+  fetch(ks, k, k_begin);
+  fetch(vs, v, k_begin);
+  for (int k0 = k_begin; k0 < k_end; k0 += FN) {
+    cp_wait<1>();
+    __syncthreads();
+    F2 s2[4][4];                                               // even and odd dims' sums
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+      for (int c = 0; c < 4; ++c) s2[i][c] = F2(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < DD; d += 4) {
-      float4 qa[4], kb[4];
+      F2 qa[4][2], kb[4][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const float4*>(qs + (ty * 4 + i) * P + d);
+      for (int i = 0; i < 4; ++i) ld_pairs(qs + (ty * 4 + i) * P + d, qa[i]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) kb[c] = *reinterpret_cast<const float4*>(ks + (tx + 16 * c) * P + d);
+      for (int c = 0; c < 4; ++c) ld_pairs(ks + (tx + 16 * c) * P + d, kb[c]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          s[i][c] = fmaf(qa[i].x, kb[c].x, s[i][c]);
-          s[i][c] = fmaf(qa[i].y, kb[c].y, s[i][c]);
-          s[i][c] = fmaf(qa[i].z, kb[c].z, s[i][c]);
-          s[i][c] = fmaf(qa[i].w, kb[c].w, s[i][c]);
-        }
+        for (int c = 0; c < 4; ++c) s2[i][c] = fma2(qa[i][1], kb[c][1], fma2(qa[i][0], kb[c][0], s2[i][c]));
     }
+    __syncthreads();
+    fetch(ks, k, k0 + FN);
+    // scores; a row's max is moved only once a score passes it by 2^8
+    float s[4][4];
+    bool grow = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int pos = a.n_kv - a.n_q + row0 + ty * 4 + i;
-      float mx = m[i];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int key = k0 + tx + 16 * c;
-        float z = s[i][c] * scale;
-        if (cap) z = a.softcap * tanhf(z * inv_cap);
+        float z0, z;
+        s2[i][c].get(&z0, &z);
+        z = (z0 + z) * scale;
+        if (cap) z = a.softcap * tanh_f32(z * inv_cap);
         z = fmaf(-slope, fabsf((float)(pos - key)), z) * kLog2e;
         s[i][c] = key >= lo[i] && key < hi[i] ? z : -INFINITY;
-        mx = fmaxf(mx, s[i][c]);
+        grow |= s[i][c] > m[i] + kRescaleLog2;                 // also from m = -inf
       }
+    }
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-      for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-      const float mb = mx == -INFINITY ? 0.f : mx;
-      const float al = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - mb);
-      m[i] = mx;
-      float sum = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+#pragma unroll
+        for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        mx = fmaxf(mx, m[i]);
+        const float al = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - mx);
+        m[i] = mx;
+        l[i] *= al;
+#pragma unroll
+        for (int e = 0; e < DV; ++e) o[i][e] = mul2(o[i][e], F2(al, al));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float mb = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float p = ex2_approx(s[i][c] - mb);
-        sum += p;
+        l[i] += p;                                             // of this thread's columns
         ps[(ty * 4 + i) * SP + tx + 16 * c] = p;
       }
-#pragma unroll
-      for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      l[i] = fmaf(l[i], al, sum);
-#pragma unroll
-      for (int e = 0; e < 2 * DV; ++e) o[i][e] *= al;
     }
-    __syncwarp();                                              // a row's 16 threads share a warp
-    if (!odd) {
-#pragma unroll 2
+    cp_wait<1>();
+    float zero = 0.f;                                          // NaN with a non-finite V element here
+#pragma unroll 4
+    for (int x = tid; x < FN * (DD / 4); x += FTHREADS) {      // (the pieces that this thread fetched)
+      const float4 f = *reinterpret_cast<const float4*>(vs + x / (DD / 4) * P + x % (DD / 4) * 4);
+      zero = fmaf(f.x, 0.f, fmaf(f.y, 0.f, fmaf(f.z, 0.f, fmaf(f.w, 0.f, zero))));
+    }
+    if (!__syncthreads_or(zero != 0.f)) {
+#pragma unroll 4
       for (int kk = 0; kk < FN; kk += 4) {
         float4 p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(ps + (ty * 4 + i) * SP + kk);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
+          F2 vv[DV];
 #pragma unroll
-          for (int e = 0; e < DV; ++e) {
-            const float2 vv = *reinterpret_cast<const float2*>(vs + (kk + x) * P + 2 * tx + 32 * e);
+          for (int e = 0; e < DV; ++e) vv[e] = *reinterpret_cast<const F2*>(vs + (kk + x) * P + 2 * tx + 32 * e);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float pw = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
-              o[i][2 * e] = fmaf(pw, vv.x, o[i][2 * e]);
-              o[i][2 * e + 1] = fmaf(pw, vv.y, o[i][2 * e + 1]);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
+#pragma unroll
+            for (int e = 0; e < DV; ++e) o[i][e] = fma2(F2(w, w), vv[e], o[i][e]);
           }
         }
       }
@@ -1076,28 +1123,35 @@ __global__ void __launch_bounds__(FTHREADS)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (k0 + kk < lo[i] || k0 + kk >= hi[i]) continue;
-          const float pw = ps[(ty * 4 + i) * SP + kk];
+          const float w = ps[(ty * 4 + i) * SP + kk];
+          const F2 pw(w, w);
 #pragma unroll
-          for (int e = 0; e < DV; ++e) {
-            const float2 vv = *reinterpret_cast<const float2*>(vs + kk * P + 2 * tx + 32 * e);
-            o[i][2 * e] = fmaf(pw, vv.x, o[i][2 * e]);
-            o[i][2 * e + 1] = fmaf(pw, vv.y, o[i][2 * e + 1]);
-          }
+          for (int e = 0; e < DV; ++e)
+            o[i][e] = fma2(pw, *reinterpret_cast<const F2*>(vs + kk * P + 2 * tx + 32 * e), o[i][e]);
         }
     }
+    __syncthreads();
+    fetch(vs, v, k0 + FN);
   }
+  cp_wait<0>();
   float* out = (n_splits > 1 ? o_part + (size_t)split * a.n_q * ldq : reinterpret_cast<float*>(a.o)) + (size_t)h * DD;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = row0 + ty * 4 + i;
-    if (row >= a.n_q) continue;
-    const bool have = l[i] > 0.f || l[i] != l[i];
+    float sum = l[i];
 #pragma unroll
-    for (int e = 0; e < DV; ++e)
+    for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    if (row >= a.n_q) continue;
+    const bool have = sum > 0.f || sum != sum;
+#pragma unroll
+    for (int e = 0; e < DV; ++e) {
+      float o0, o1;
+      o[i][e].get(&o0, &o1);
       *reinterpret_cast<float2*>(out + (size_t)row * ldq + 2 * tx + 32 * e) =
-          have ? make_float2(o[i][2 * e] / l[i], o[i][2 * e + 1] / l[i]) : make_float2(0.f, 0.f);
+          have ? make_float2(o0 / sum, o1 / sum) : make_float2(0.f, 0.f);
+    }
     if (n_splits > 1 && tx == 0)
-      lse_part[((size_t)split * a.n_q + row) * a.heads + h] = have ? m[i] + log2f(l[i]) : -INFINITY;
+      lse_part[((size_t)split * a.n_q + row) * a.heads + h] = have ? m[i] + log2f(sum) : -INFINITY;
   }
 }
 
@@ -1121,19 +1175,32 @@ long long base_ctas(int n_q, int heads, int kv_heads) {
 
 }  // namespace
 
-// Splits fill the SMs when the query blocks alone do not.  bf16: one CTA per SM, each at
-// least two key tiles of the longest possible range; fp32: four per SM, each at least four.
-int masked_splits(int n_q, int n_kv, int heads, int kv_heads, int dtype) {
+// Key splits when the query blocks alone do not fill the SMs (bf16: one CTA on each, fp32: four):
+// as many as cost least, counting a split's key tiles of the longest possible range (2 us each,
+// fp32 3.4), the join (3.5 us) and the partials (written and read, 4 TB/s).  Against "at least two
+// tiles a split (fp32: four), at most 16": 1 query over 2,148 keys, 1 head 12.9 -> 10.5 us, over
+// 30,000 37 -> 25; 300 queries over themselves, 24 heads: no splits either way.
+int masked_splits(int n_q, int n_kv, int heads, int kv_heads, int head_dim, int dtype) {
   const bool tc = dtype == SFM_DTYPE_BF16;
   const long long ctas = tc ? base_ctas(n_q, heads, kv_heads) : (long long)((n_q + FM - 1) / FM) * heads;
-  const int tiles = tc ? (n_kv + BKV - 1) / BKV / 2 : (n_kv + FN - 1) / FN / 4;
-  const long long want = (tc ? kSms : 4 * kSms) / ctas;
-  const int s = want < tiles ? (int)want : tiles;
-  return s < 1 ? 1 : s > kMaxKeySplits ? kMaxKeySplits : s;
+  const int tiles = tc ? (n_kv + BKV - 1) / BKV : (n_kv + FN - 1) / FN;
+  const long long room = (tc ? kSms : 4 * kSms) / ctas;
+  const int most = (int)(room < kMaxKeySplits ? room : kMaxKeySplits);
+  const double tile = tc ? 2.0 : 3.4, part = 8e-6 / 4.0 * (head_dim + 1.0) * n_q * heads;
+  double best = tile * tiles;
+  int splits = 1;
+  for (int s = 2; s <= most && s <= tiles; ++s) {
+    const double cost = tile * ((tiles + s - 1) / s) + 3.5 + part * s;
+    if (cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  return splits;
 }
 
 size_t masked_workspace(int n_q, int n_kv, int heads, int kv_heads, int head_dim, int dtype) {
-  const int sp = masked_splits(n_q, n_kv, heads, kv_heads, dtype);
+  const int sp = masked_splits(n_q, n_kv, heads, kv_heads, head_dim, dtype);
   if (sp == 1) return 0;
   const size_t b = (size_t)sp * n_q * heads * (head_dim + 1) * sizeof(float);
   return (b + 15) / 16 * 16;
@@ -1147,7 +1214,7 @@ int launch_attention_masked_tc(const MaskedArgs& a, const CUtensorMap& mq, const
   t.hgroups = t.paired ? a.heads / 2 : a.heads;
   const int rows = t.paired ? BQ : 2 * BQ;
   t.qblocks = (a.n_q + rows - 1) / rows;
-  t.n_splits = masked_splits(a.n_q, a.n_kv, a.heads, a.kv_heads, SFM_DTYPE_BF16);
+  t.n_splits = masked_splits(a.n_q, a.n_kv, a.heads, a.kv_heads, D, SFM_DTYPE_BF16);
   const long long rows_heads = (long long)a.n_q * a.heads;
   if (t.n_splits > 1) {
     t.o_part = (float*)workspace;
@@ -1172,7 +1239,7 @@ int launch_attention_masked_tc(const MaskedArgs& a, const CUtensorMap& mq, const
 }
 
 int launch_attention_masked_f32(const MaskedArgs& a, void* workspace, cudaStream_t s) {
-  const int n_splits = masked_splits(a.n_q, a.n_kv, a.heads, a.kv_heads, SFM_DTYPE_FP32);
+  const int n_splits = masked_splits(a.n_q, a.n_kv, a.heads, a.kv_heads, a.head_dim, SFM_DTYPE_FP32);
   const long long rows_heads = (long long)a.n_q * a.heads;
   float *o_part = nullptr, *lse_part = nullptr;
   if (n_splits > 1) {

@@ -21,7 +21,7 @@ struct MaskedArgs {
 };
 
 // Key splits of a call (a function of the shape alone) and the scratch they need.
-int masked_splits(int n_q, int n_kv, int heads, int kv_heads, int dtype);
+int masked_splits(int n_q, int n_kv, int heads, int kv_heads, int head_dim, int dtype);
 size_t masked_workspace(int n_q, int n_kv, int heads, int kv_heads, int head_dim, int dtype);
 int launch_attention_masked_tc(const MaskedArgs& a, const CUtensorMap& mq, const CUtensorMap& mk,
                                const CUtensorMap& mv, void* workspace, const Guard& gd, cudaStream_t s);

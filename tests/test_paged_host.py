@@ -134,5 +134,5 @@ def test_workspaces():
     mk = L.lib.sfm_attention_masked_workspace_bytes
     assert mk(4096, 4096, 24, 8, 128, BF) == 0                # enough query blocks: no splits
     assert mk(1, 40000, 8, 8, 128, BF) > 0
-    assert mk(1, 40000, 8, 8, 64, F32) > 0 and mk(1, 200, 8, 8, 64, F32) == 0
+    assert mk(1, 40000, 8, 8, 64, F32) > 0 and mk(1, 64, 8, 8, 64, F32) == 0
     assert C.sizeof(C.c_size_t) == 8
