@@ -7,9 +7,9 @@
 //
 // bf16 (D = 128) runs on the tensor cores (tcgen05), bound by them and by the softmax
 // beside them.  One CTA = two 128-row query tiles over the same key tiles: two heads of
-// one group at the same rows where the group is even (both tiles then have the same
-// ranges and no key tile is loaded for the sake of one of them), else 256 rows of one
-// head.  384 threads:
+// one group at the same rows (both tiles then have the same ranges and no key tile is
+// loaded for the sake of one of them), and for an odd group's last head 256 of its rows.
+// 384 threads:
 //   warp 0      TMA producer: the Q tiles once, K tiles (128 keys) in a 3-stage ring, V
 //               tiles in a 2-stage ring (128-byte swizzle)
 //   warp 1      TMEM allocator; one lane issues S_t = Q_t K_j^T and O_t += P_t V_j (P from
@@ -24,13 +24,15 @@
 // The CTA's key tiles are those that the union of its rows' ranges touches (a reduction
 // over the rows' bounds at the start; nothing outside is loaded); a tile inside every
 // row's range is not masked.  The last query blocks go first in the grid: under a causal
-// mask they have the most keys.
+// mask they have the most keys; within a block the key heads go round first, so that CTAs
+// of equal work are neighbours (8,192 packed, 3 heads a group: 192 -> 186 us; the pairs'
+// CTAs of one key head side by side: 204).
 // Few query rows over many keys: the key tiles are cut into splits whose fp32 partials a
 // second kernel joins.
 //
 // Measured (bf16): a block's 256 rows over 128 keys take ~1.9 us in the steady state, 1.3
 // PFLOP/s, the softmax as long as the products beside it; set-up and output of a block 6 to 9
-// us.  8,192 packed causal queries of 24 heads, cap 50: 194 us (172 without the cap); 8,000 with
+// us.  8,192 packed causal queries of 24 heads, cap 50: 186 us (166 without the cap); 8,000 with
 // prefixes and a bias: 418 us (393 without); 48 queries over 2,148 keys: 17 us.
 //
 // fp32 runs on the CUDA cores in 32 x 64 tiles: 1,000 queries over 1,400 keys, 4 heads, D 64, in
@@ -107,9 +109,9 @@ constexpr int kSms = 148;
 
 struct TcArgs {
   MaskedArgs m;
-  int paired;          // the CTA's tiles: 1 = two heads of a group, 0 = two row blocks of a head
-  int hgroups;         // heads (or pairs of heads)
-  int qblocks;         // row blocks per head group
+  int halves;          // 128-row blocks in a row block of the grid: 2 where an odd head takes both
+  int units;           // CTAs of a key head and row block: the pairs of heads, block by block, an odd head
+  int qblocks;         // row blocks
   int n_splits;
   float* o_part;       // [split][n_q][H][D]
   float* lse_part;     // [split][n_q][H] (log2)
@@ -224,15 +226,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   const MaskedArgs& m_ = args.m;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int rem = blockIdx.x;
-  const int hg = rem % args.hgroups;
-  rem /= args.hgroups;
+  const int hk = rem % m_.kv_heads;
+  rem /= m_.kv_heads;
+  const int unit = rem % args.units;
+  rem /= args.units;
   const int split = rem % args.n_splits;
   const int qb = args.qblocks - 1 - rem / args.n_splits;
-  const int h_a = args.paired ? 2 * hg : hg;                   // head of tile A
-  const int dh = args.paired ? 1 : 0;                          // tile B: head h_a + dh,
-  const int dr = args.paired ? 0 : BQ;                         //         rows + dr
-  const int row0 = qb * (args.paired ? BQ : 2 * BQ);
-  const int hk = h_a / (m_.heads / m_.kv_heads);
+  const int G = m_.heads / m_.kv_heads;
+  const bool paired = unit < G / 2 * args.halves;
+  const int h_a = hk * G + (paired ? unit / args.halves * 2 : G - 1);       // head of tile A
+  const int dh = paired ? 1 : 0;                               // tile B: head h_a + dh,
+  const int dr = paired ? 0 : BQ;                              //         rows + dr
+  const int row0 = (qb * args.halves + (paired ? unit % args.halves : 0)) * BQ;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // max then hardly moves, where in ascending order it would in every tile of a steep head.
   int near = 0;
   if (BIAS && T > 0) {
-    const int pos = m_.n_kv - m_.n_q + min(row0 + (args.paired ? BQ : 2 * BQ), m_.n_q) - 1;
+    const int pos = m_.n_kv - m_.n_q + min(row0 + dr + BQ, m_.n_q) - 1;
     near = min(max(pos / BKV - t0, 0), T - 1);
   }
   auto tile_at = [&](int i) { return !BIAS ? t0 + i : t0 + (i <= near ? near - i : i); };
@@ -1165,12 +1170,23 @@ cudaError_t run_f32(const MaskedArgs& a, int n_splits, float* o_part, float* lse
   return launch_dependent(attn_masked_f32_kernel<DV>, grid, FTHREADS, smem, s, a, n_splits, o_part, lse_part);
 }
 
-bool pairs_heads(int heads, int kv_heads) { return (heads / kv_heads) % 2 == 0; }
+// The grid over rows and heads (see TcArgs): an odd group's last head takes 256 rows at a time,
+// its pairs 128, so their row blocks are twice as many where there is more than one.
+struct Cover {
+  int halves, units, qblocks;
+};
+Cover cover(int n_q, int heads, int kv_heads) {
+  const int g = heads / kv_heads, blocks = (n_q + BQ - 1) / BQ;
+  Cover c;
+  c.halves = g % 2 && blocks > 1 ? 2 : 1;
+  c.units = g / 2 * c.halves + g % 2;
+  c.qblocks = (blocks + c.halves - 1) / c.halves;
+  return c;
+}
 
 long long base_ctas(int n_q, int heads, int kv_heads) {
-  const bool p = pairs_heads(heads, kv_heads);
-  const int rows = p ? BQ : 2 * BQ;
-  return (long long)((n_q + rows - 1) / rows) * (p ? heads / 2 : heads);
+  const Cover c = cover(n_q, heads, kv_heads);
+  return (long long)c.qblocks * c.units * kv_heads;
 }
 
 }  // namespace
@@ -1210,10 +1226,10 @@ int launch_attention_masked_tc(const MaskedArgs& a, const CUtensorMap& mq, const
                                const CUtensorMap& mv, void* workspace, const Guard& gd, cudaStream_t s) {
   TcArgs t{};
   t.m = a;
-  t.paired = pairs_heads(a.heads, a.kv_heads) ? 1 : 0;
-  t.hgroups = t.paired ? a.heads / 2 : a.heads;
-  const int rows = t.paired ? BQ : 2 * BQ;
-  t.qblocks = (a.n_q + rows - 1) / rows;
+  const Cover c = cover(a.n_q, a.heads, a.kv_heads);
+  t.halves = c.halves;
+  t.units = c.units;
+  t.qblocks = c.qblocks;
   t.n_splits = masked_splits(a.n_q, a.n_kv, a.heads, a.kv_heads, D, SFM_DTYPE_BF16);
   const long long rows_heads = (long long)a.n_q * a.heads;
   if (t.n_splits > 1) {
@@ -1231,7 +1247,7 @@ int launch_attention_masked_tc(const MaskedArgs& a, const CUtensorMap& mq, const
   int rc;
   {
     ProfScope ps(SFM_PROF_ATTN, s);
-    rc = record_cuda(launch_dependent(kernel, (unsigned)(t.qblocks * t.hgroups * t.n_splits), THREADS, SMEM, s, mq, mk,
+    rc = record_cuda(launch_dependent(kernel, (unsigned)(t.qblocks * t.units * a.kv_heads * t.n_splits), THREADS, SMEM, s, mq, mk,
                                       mv, t));
   }
   if (rc || t.n_splits == 1) return rc;

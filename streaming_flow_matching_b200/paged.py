@@ -179,7 +179,7 @@ def attention_bounds(n_q, n_kv, *, doc_starts=None, prefixes=None, causal=False,
     """
     dev = _device()
     n_docs = doc_starts.numel() - 1 if doc_starts is not None else (1 if prefixes is not None else 0)
-    lo, hi = _empty((2, n_q), dtype=_I32, device=dev).unbind() if out is None else out
+    lo, hi = (_empty(n_q, dtype=_I32, device=dev), _empty(n_q, dtype=_I32, device=dev)) if out is None else out
     L.check(_bounds(
         n_q, n_kv, 0 if doc_starts is None else _ptr(doc_starts, _I32, "doc_starts", (n_docs + 1,), dev),
         0 if prefixes is None else _ptr(prefixes, _I32, "prefixes", (n_docs,), dev), n_docs, 1 if causal else 0,

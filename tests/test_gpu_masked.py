@@ -221,6 +221,16 @@ def test_more_blocks_than_sms(cuda_device, h, hk):
     assert int(torch.count_nonzero(out[0])) == 0
 
 
+@pytest.mark.parametrize("h,hk", [(3, 1), (6, 2), (5, 1), (14, 2), (7, 7)])
+@pytest.mark.parametrize("n_q,n_kv", [(100, 700), (128, 128), (129, 129), (256, 900), (300, 300), (700, 700)])
+def test_odd_groups(cuda_device, h, hk, n_q, n_kv):
+    # pairs of heads and the odd one cover rows differently: every head and row once, in splits too
+    from streaming_flow_matching_b200 import attention_bounds
+    q, k, v = make(n_q, n_kv, h, hk, 128, BF, seed=h + n_q)
+    lo, hi = attention_bounds(n_q, n_kv, doc_starts=ints([0, n_kv // 3, n_kv // 2, n_kv]), causal=True)
+    run(q, k, v, lo, hi, softcap=20.0, slopes=ladder(h))
+
+
 @pytest.mark.parametrize("h,hk", [(1, 1), (3, 1), (4, 2)])
 @pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, True)])
 def test_query_tiles_with_their_own_keys(cuda_device, h, hk, cap, bias):
