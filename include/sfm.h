@@ -500,10 +500,10 @@ SFM_API int sfm_paged_append(const void* k, const void* v, void* k_pages, void* 
  *   weights[s][h_kv][t] += sum of softmax(s)_t over the query heads of h_kv
  * lengths counts the slots to attend to (the new token's own, once appended,
  * included).  o is a buffer other than q (SFM_EINVAL).  positions and q_positions
- * go together and need slopes.  Any number of query heads per key head.  Results do
- * not depend on timing (partials are joined in a fixed order).  workspace: the size
- * for max_tokens = max_pages * page_size, or cap where that is smaller and the call
- * has state arrays.
+ * go together; without slopes they are not read.  Any number of query heads per key
+ * head.  Results do not depend on timing (partials are joined in a fixed order).
+ * workspace: the size for max_tokens = max_pages * page_size, or cap where that is
+ * smaller and the call has state arrays.
  */
 SFM_API size_t sfm_paged_attention_workspace_bytes(int n_seq, int max_tokens, int n_heads,
                                                    int n_kv_heads, int head_dim, int dtype,

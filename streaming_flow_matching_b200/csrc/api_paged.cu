@@ -111,8 +111,7 @@ int sfm_paged_attention(const void* q, const void* k_pages, const void* v_pages,
   if (!q || !o || o == q || !aligned(q, 16) || !aligned(o, 16)) return SFM_EINVAL;
   if (!cap_ok(softcap)) return SFM_EINVAL;
   const bool state = positions || weights;
-  if ((state && cap < 1) || ((positions != nullptr) != (q_positions != nullptr)) || (positions && !slopes))
-    return SFM_EINVAL;
+  if ((state && cap < 1) || ((positions != nullptr) != (q_positions != nullptr))) return SFM_EINVAL;
   if (!aligned(slopes, 4) || !aligned(positions, 4) || !aligned(q_positions, 4) || !aligned(weights, 4))
     return SFM_EINVAL;
   DecodeArgs a{};
@@ -134,8 +133,8 @@ int sfm_paged_attention(const void* q, const void* k_pages, const void* v_pages,
   a.heads = n_heads;
   a.softcap = softcap;
   a.slopes = slopes;
-  a.positions = positions;
-  a.q_positions = q_positions;
+  a.positions = slopes ? positions : nullptr;      // only the bias looks at them
+  a.q_positions = slopes ? q_positions : nullptr;
   a.weights = weights;
   a.cap = cap;
   a.err = gd.err;

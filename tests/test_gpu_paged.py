@@ -221,6 +221,18 @@ def test_attention_positions(cuda_device, dtype, d):
         weights=torch.zeros(3, hk, 705, device="cuda"))
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_positions_without_a_bias_change_nothing(cuda_device, dtype, d):
+    from streaming_flow_matching_b200 import paged_attention
+    lens = [300, 1, 77]
+    c = Cache(lens, 16, 2, d, dtype, seed=8)
+    q = torch.randn(3, 6, d, device="cuda").to(dtype)
+    pos = torch.randint(0, 9999, (3, 2, 300), dtype=torch.int32, device="cuda")
+    w = torch.zeros(3, 2, 300, device="cuda")
+    a = paged_attention(q, c.k, c.v, c.table, ints(lens), positions=pos, q_positions=ints([9999] * 3), weights=w)
+    assert torch.equal(a, run(c, q, lens, weights=torch.zeros_like(w)))
+
+
 def test_attention_many_sequences(cuda_device):
     # more sequences than a warp scans at once, and than CTA slots; runs of empty ones
     r = random.Random(2)
@@ -575,7 +587,7 @@ def test_refusals(cuda_device):
         (lambda: paged_attention(q, c.k.transpose(0, 1), c.v, c.table, lens), ValueError),
         (lambda: paged_attention(q, c.k, c.v, c.table, lens, softcap=-2.0), L.SfmError),
         (lambda: paged_attention(q, c.k, c.v, c.table, lens, slopes=sl, positions=pos), L.SfmError),
-        (lambda: paged_attention(q, c.k, c.v, c.table, lens, positions=pos, q_positions=lens), L.SfmError),
+        (lambda: paged_attention(q, c.k, c.v, c.table, lens, q_positions=lens), L.SfmError),
         (lambda: paged_attention(q, c.k, c.v, c.table, lens, weights=w[:, :1].contiguous()), ValueError),
         (lambda: paged_attention(q, c.k, c.v, c.table, lens, weights=w.double()), ValueError),
         (lambda: paged_attention(q, c.k, c.v, c.table, lens,

@@ -68,7 +68,7 @@ def test_append_arguments(bad):
 @pytest.mark.parametrize("bad", [
     dict(q=None), dict(o=None), dict(o=P), dict(q=P + 8), dict(o=P + 2), dict(h=3), dict(h=0), dict(cap=-1.0),
     dict(cap=INF), dict(cap=1e-4), dict(cap=1e31),
-    dict(cap=NAN), dict(positions=None), dict(q_positions=None), dict(slopes=None), dict(room=0), dict(ws=None),
+    dict(cap=NAN), dict(positions=None), dict(q_positions=None), dict(room=0), dict(ws=None),
     dict(ws=P + 8), dict(ws_bytes=16), dict(slopes=P + 2)])
 def test_attention_arguments(bad):
     assert attention(**bad) == L.SFM_EINVAL
