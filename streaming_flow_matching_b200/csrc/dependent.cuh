@@ -20,21 +20,31 @@ __device__ __forceinline__ void grid_dependency_trigger() {
 }
 #endif
 
-// Launches a kernel that may be set up while the previous one in the stream still runs.
+// Launches a kernel that may be set up while the previous one in the stream still runs, its CTAs
+// in clusters of that size.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
-                             cudaStream_t s, A... args) {
+cudaError_t launch_dependent_clusters(void (*kernel)(P...), int cluster, unsigned grid, unsigned block, size_t smem,
+                                      cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                             A... args) {
+  return launch_dependent_clusters(kernel, 1, grid, block, smem, s, args...);
 }
 
 }  // namespace sfm

@@ -12,18 +12,22 @@
 // that lie at slots >= keep move into the evicted slots < keep, both in ascending
 // order, and no other row is touched.  Sources and destinations are disjoint, so
 // the moves run in any order.  Two kernels:
-//   select  one CTA per (sequence, key head): the keep-th largest rank by radix
-//           selection (digits of 11, 11 and 10 bits, a histogram each), then the
-//           lists of evicted slots < keep and kept slots >= keep in slot order
+//   select  one CTA, or a cluster of 2 to 8, per (sequence, key head): the keep-th
+//           largest rank by radix selection (digits of 11, 11 and 10 bits, a histogram
+//           each), then the lists of evicted slots < keep and kept slots >= keep in slot
+//           order.  The CTAs of a cluster take a run of slots each and read one another's
+//           histograms and counts.
 //   move    a warp per 8 moved rows (K and V rows of one head, weight, position)
 //
 // Measured (bf16): append of 8 x ~1,150 rows of 24 heads 38.7 us, 5.9 TB/s (0.89 of a copy's
 // rate).  Eviction of 16 sequences x 8 heads from 30,500-36,000 to 30,000 slots 110 us: select 31 us,
 // bound by its instructions (62 % issue); moves 70 us, bound by memory at 256 bytes a piece;
-// of 4 x 1,200 to 924: 14 us, latency.
+// of 4 x 1,200 to 924: 14 us, latency.  (Select alone with few moves, one sequence of 57,600:
+// 24 heads 31 us.)
 #include <limits.h>
 
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace sfm {
 
@@ -98,6 +102,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBatch = 8;       // loads in flight per thread
 constexpr int kHeldRanks = 48 * 1024;   // ranks in shared memory: 192 KB
+constexpr int kSms = 148;
 
 // Rank of a token as an unsigned number, larger = kept first: NaN below every number,
 // -0 equal to +0, protected tokens above all.
@@ -115,26 +120,56 @@ __device__ __forceinline__ int warp_sum(int v) {
 }
 
 // lists: per (sequence, key head) `room` evicted slots then `room` moved slots; counts: one each.
-// The ranks are made once and kept in shared memory (`held` of them at most; a longer
-// sequence makes them again in each of its five passes).  Bound by instructions: one CTA
-// handles one sequence and key head, so the passes over shared memory are kept short.
-struct SelectShared {
-  unsigned hist[kBins];
+// The ranks are made once and kept in shared memory (`held` of them at most; a longer run of
+// slots makes them again in each of its passes).  Bound by instructions: a CTA passes over its
+// slots five times, so those passes over shared memory are kept short.
+// slots of each CTA of a cluster, whole warps of them
+__host__ __device__ inline int select_run(int n, int parts) { return ((n + parts - 1) / parts + 31) & ~31; }
+
+struct __align__(8) SelectShared {
+  unsigned hist[3][kBins];      // one for each digit: none is cleared while another CTA reads it
   int part[3][kSelWarps];
+  int total[4];                 // of this CTA: newest position, ties, evicted, moved
   unsigned digit;
   int above;
 };
 
+// All threads of the cluster (or of the CTA that is alone); what they wrote to shared memory is seen.
+__device__ __forceinline__ void cluster_barrier(int parts) {
+  if (parts == 1) __syncthreads();
+  else sm100::cluster_sync();
+}
+// A word of shared memory at the place of `p` in CTA `rank` of the cluster.
+__device__ __forceinline__ unsigned peer_word(const void* p, int rank) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];"
+               : "=r"(v)
+               : "r"(sm100::mapa_shared(sm100::smem_u32(p), (uint32_t)rank))
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint2 peer_words(const void* p, int rank) {          // 8 bytes
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "r"(sm100::mapa_shared(sm100::smem_u32(p), (uint32_t)rank))
+               : "memory");
+  return v;
+}
+
 template <bool HOLD>
 __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict__ counts, int* __restrict__ lists,
-                                             int room, int n, SelectShared& sh) {
+                                             int room, int item, int part_id, int parts, int from, int n,
+                                             SelectShared& sh) {
   extern __shared__ unsigned ranks[];
-  auto& hist = sh.hist;
   auto& part = sh.part;
-  const int item = blockIdx.x, keep = a.keep;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const float* w = a.weights + (size_t)item * a.cap;
-  const int* pos = a.positions + (size_t)item * a.cap;
+  // this CTA's slots: from, ... from + n - 1 (none, at the end of a short sequence)
+  const int keep = a.keep - from;
+  const float* w = a.weights + (size_t)item * a.cap + from;
+  const int* pos = a.positions + (size_t)item * a.cap + from;
+  for (int b = tid; b < 3 * kBins; b += kSelThreads) sh.hist[0][b] = 0;
   // newest position
   int mx = INT_MIN;
   for (int t0 = tid; t0 < n; t0 += kBatch * kSelThreads) {
@@ -148,7 +183,11 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
   if (lane == 0) part[0][warp] = mx;
   __syncthreads();
   mx = __reduce_max_sync(0xffffffffu, part[0][lane]);
-  __syncthreads();
+  if (parts > 1) {
+    if (tid == 0) sh.total[0] = mx;
+    cluster_barrier(parts);
+    mx = __reduce_max_sync(0xffffffffu, lane < parts ? (int)peer_word(&sh.total[0], lane) : INT_MIN);
+  }
   const int recent_from = (int)max((long long)INT_MIN, (long long)mx - a.n_recent + 1);   // (n_recent > 0)
   auto make_rank = [&](int t) { return rank_of(__ldg(w + t), __ldg(pos + t), a.n_first, a.n_recent > 0, recent_from); };
   auto rank = [&](int t) { return HOLD ? ranks[t] : make_rank(t); };
@@ -156,12 +195,11 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
   // prefix found so far are still to be taken.  The first digit is counted as the
   // ranks are made.
   unsigned prefix = 0, mask = 0;
-  int want = keep;
+  int want = a.keep;
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
     const unsigned bins = d == 2 ? 1024u : 2048u;
-    for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
-    __syncthreads();
+    unsigned* hist = sh.hist[d];
     if (d == 0) {
       for (int t0 = tid; t0 < n; t0 += kBatch * kSelThreads) {
         float wv[kBatch];
@@ -187,9 +225,21 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
         if ((r & mask) == prefix) atomicAdd(&hist[(r >> shift) & (bins - 1)], 1u);
       }
     }
-    __syncthreads();
+    cluster_barrier(parts);
     // bins from the top: thread i holds bins (2047 - 2 i), (2046 - 2 i)
-    const int c0 = (int)hist[kBins - 1 - 2 * tid], c1 = (int)hist[kBins - 2 - 2 * tid];
+    const int b0 = kBins - 2 - 2 * tid;
+    int c0 = 0, c1 = 0;
+    if (parts == 1) {
+      c0 = (int)hist[b0 + 1];
+      c1 = (int)hist[b0];
+    } else {
+#pragma unroll 8
+      for (int r = 0; r < parts; ++r) {
+        const uint2 c = peer_words(&hist[b0], r);
+        c0 += (int)c.y;
+        c1 += (int)c.x;
+      }
+    }
     int inc = c0 + c1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -201,10 +251,10 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
     const int before = warp_sum(lane < warp ? part[0][lane] : 0);
     const int exc = before + inc - c0 - c1;
     if (exc < want && want <= exc + c0) {
-      sh.digit = kBins - 1 - 2 * tid;
+      sh.digit = b0 + 1;
       sh.above = exc;
     } else if (exc + c0 < want && want <= exc + c0 + c1) {
-      sh.digit = kBins - 2 - 2 * tid;
+      sh.digit = b0;
       sh.above = exc + c0;
     }
     __syncthreads();
@@ -238,7 +288,13 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
   n_mv = warp_sum(n_mv);
   if (lane == 0) part[0][warp] = tie_lo + tie_hi;
   __syncthreads();
-  const int tie_base = warp_sum(lane < warp ? part[0][lane] : 0);
+  int tie_base = warp_sum(lane < warp ? part[0][lane] : 0);
+  if (parts > 1) {                                             // and the CTAs before
+    const int all = warp_sum(part[0][lane]);
+    if (tid == 0) sh.total[1] = all;
+    cluster_barrier(parts);
+    tie_base += warp_sum(lane < part_id ? (int)peer_word(&sh.total[1], lane) : 0);
+  }
   const int left = max(0, want - tie_base);                    // ties of this run that stay
   n_out += max(0, tie_lo - left);
   n_mv += min(tie_hi, max(0, left - tie_lo));
@@ -248,12 +304,22 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
   }
   __syncthreads();
   int no = warp_sum(lane < warp ? part[1][lane] : 0), nm = warp_sum(lane < warp ? part[2][lane] : 0);
+  if (parts > 1) {
+    const int all_o = warp_sum(part[1][lane]), all_m = warp_sum(part[2][lane]);
+    if (tid == 0) {
+      sh.total[2] = all_o;
+      sh.total[3] = all_m;
+    }
+    cluster_barrier(parts);
+    no += warp_sum(lane < part_id ? (int)peer_word(&sh.total[2], lane) : 0);
+    nm += warp_sum(lane < part_id ? (int)peer_word(&sh.total[3], lane) : 0);
+  }
   int* outs = lists + (size_t)item * 2 * room;
   int* mvs = outs + room;
   const unsigned lower = (1u << lane) - 1u;
   int tie = tie_base;
-  auto walk = [&](int from, int to, bool behind, int* list, int at) {
-    for (int t = from; t < to; t += 32 * kBatch) {
+  auto walk = [&](int begin, int to, bool behind, int* list, int at) {
+    for (int t = begin; t < to; t += 32 * kBatch) {
       unsigned rv[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
@@ -272,7 +338,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
         }
         const bool take = x < to && stay == behind;
         const unsigned m = __ballot_sync(0xffffffffu, take);
-        if (take) list[at + __popc(m & lower)] = x;
+        if (take) list[at + __popc(m & lower)] = from + x;
         at += __popc(m);
       }
     }
@@ -281,22 +347,24 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
   walk(t0, mid, false, outs, no);
   nm = walk(mid, t1, true, mvs, nm);
   // as many slots were evicted before `keep` as are kept behind it
-  if (warp == kSelWarps - 1 && lane == 0) counts[item] = nm;
+  if (part_id == parts - 1 && warp == kSelWarps - 1 && lane == 0) counts[item] = nm;
+  if (parts > 1) cluster_barrier(parts);                       // nobody leaves while its words are read
 }
 
 __global__ void __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictArgs a, int* __restrict__ counts,
-                        int* __restrict__ lists, int room, int held) {
+                        int* __restrict__ lists, int room, int held, int parts) {
   __shared__ SelectShared sh;
   grid_dependency_wait();
-  const int n = cache_len(a.c, blockIdx.x / a.c.kv_heads, a.err);
-  if (n <= a.keep) {
-    if (threadIdx.x == 0) counts[blockIdx.x] = 0;
-  } else if (n <= held) {
-    evict_select<true>(a, counts, lists, room, n, sh);
-  } else {
-    evict_select<false>(a, counts, lists, room, n, sh);
+  const int item = blockIdx.x / parts, part_id = blockIdx.x - item * parts;
+  const int n = cache_len(a.c, item / a.c.kv_heads, a.err);
+  if (n <= a.keep) {                                           // the same for the whole cluster
+    if (threadIdx.x == 0 && part_id == 0) counts[item] = 0;
+    return;
   }
+  const int run = select_run(n, parts), from = min(n, part_id * run), mine = min(n - from, run);
+  if (run <= held) evict_select<true>(a, counts, lists, room, item, part_id, parts, from, mine, sh);
+  else evict_select<false>(a, counts, lists, room, item, part_id, parts, from, mine, sh);
 }
 
 // A warp moves kMoveRows rows at a time: their slots and pages are looked up by as many
@@ -382,16 +450,24 @@ int launch_paged_evict(const EvictArgs& a, int row_bytes_head, void* workspace, 
   int* counts = (int*)workspace;
   int* lists = counts + items;
   ProfScope ps(SFM_PROF_APPEND, s);
-  const int held = a.c.max_tokens < kHeldRanks ? a.c.max_tokens : kHeldRanks;
+  // CTAs per item: a slot costs one CTA 0.6 ns, a cluster of 2, 4 or 8 costs 3.6, 6.3 and some 9 us
+  // for its barriers and histograms, and clusters fill about 128 SMs: two or four where a CTA has
+  // more than 12K slots (8 heads of 30,000: 27.8 us alone, 23.7, 22.6, and with eight 23.7; of
+  // 8,000: 14.6, 17.9, 19.6, 22.2), and as many as hold the ranks (24 heads of 57,600 in passes
+  // over global memory 101 us, held by four 30.8).
+  int parts = 1;
+  while (parts < 4 && (long long)items * parts * 2 <= 128 && a.c.max_tokens / parts > 12 * 1024) parts *= 2;
+  while (parts < 8 && select_run(a.c.max_tokens, parts) > kHeldRanks) parts *= 2;
+  const int run = select_run(a.c.max_tokens, parts), held = run < kHeldRanks ? run : kHeldRanks;
   const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kHeldRanks * (int)sizeof(unsigned));
   if (e != cudaSuccess) return record_cuda(e);
-  int rc = record_cuda(launch_dependent(evict_select_kernel, (unsigned)items, kSelThreads, held * sizeof(unsigned), s, a,
-                                        counts, lists, room, held));
+  int rc = record_cuda(launch_dependent_clusters(evict_select_kernel, parts, (unsigned)(items * parts), kSelThreads,
+                                                 held * sizeof(unsigned), s, a, counts, lists, room, held, parts));
   if (rc) return rc;
   // kMoveRows rows per warp, and no more CTAs than fill the device several times over
   int blocks = (room + kMoveRows * kMoveWarps - 1) / (kMoveRows * kMoveWarps);
-  const int most = (148 * 32 + items - 1) / items;
+  const int most = (kSms * 32 + items - 1) / items;
   if (blocks > most) blocks = most;
   return record_cuda(launch_dependent(evict_move_kernel, (unsigned)(items * blocks), kMoveWarps * 32, 0, s, a,
                                       (const int*)counts, (const int*)lists, room, row_bytes_head / 16, blocks));

@@ -466,6 +466,32 @@ def test_evict_long(cuda_device):
     assert evict_case(c, lens, w, pos, 35000, 4, 1000) > 0
 
 
+@pytest.mark.parametrize("hk,lens,cap,keep", [
+    # 2, 4 (short sequences beside a long one), 4, 2, 1 and 8 CTAs a head
+    (1, [14000], 14000, 5000), (1, [26000, 3000, 13000, 12289], 26000, 2900), (2, [40000, 2100], 60000, 30000),
+    (9, [14200], 14200, 4100), (40, [14001], 14001, 8999), (1, [250000], 250000, 200000)])
+@pytest.mark.parametrize("kind", ["few values", "spread", "nan"])
+def test_evict_in_clusters(cuda_device, hk, lens, cap, keep, kind):
+    # several CTAs share a head's slots: ties that run over their borders, borders on both sides of keep
+    c = Cache(lens, 64, hk, 32, F32, seed=4)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    w = torch.rand(len(lens), hk, cap, generator=g, device="cuda")
+    if kind == "few values":
+        w = (w * 3).floor()
+    elif kind == "nan":
+        w[:, :, ::2] = float("nan")
+    pos = torch.stack([torch.randperm(cap, generator=g, device="cuda") for _ in range(len(lens) * hk)])
+    evict_case(c, lens, w, pos.view(len(lens), hk, cap).to(torch.int32), keep, 3, keep // 4)
+
+
+def test_evict_more_than_clusters_hold(cuda_device):
+    n = 400000                                               # 8 CTAs hold 393,216 ranks
+    c = Cache([n], 512, 1, 32, F32, seed=5)
+    w = torch.rand(1, 1, n, device="cuda")
+    pos = torch.arange(n, device="cuda", dtype=torch.int32).view(1, 1, n).contiguous()
+    assert evict_case(c, [n], w, pos, 390000, 4, 1000) > 0
+
+
 def test_evict_bad_page_is_reported(cuda_device):
     from streaming_flow_matching_b200 import paged_evict
     c = Cache([64], 16, 1, 128, BF)
