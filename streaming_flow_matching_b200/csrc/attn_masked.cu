@@ -1191,24 +1191,31 @@ long long base_ctas(int n_q, int heads, int kv_heads) {
 
 }  // namespace
 
-// Key splits when the query blocks alone do not fill the SMs (bf16: one CTA on each, fp32: four):
-// as many as cost least, counting a split's key tiles of the longest possible range (2 us each,
-// fp32 3.4), the join (3.5 us) and the partials (written and read, 4 TB/s).  Against "at least two
-// tiles a split (fp32: four), at most 16": 1 query over 2,148 keys, 1 head 12.9 -> 10.5 us, over
-// 30,000 37 -> 25; 300 queries over themselves, 24 heads: no splits either way.
+// Key splits, as many as cost least: a split's key tiles of the longest possible range (2 us each,
+// fp32 3.4) and, bf16, a CTA's set-up and output (7 us), in every wave of CTAs; the join (3.5 us)
+// and the partials (written and read, 4 TB/s).  bf16 runs one CTA on an SM, so that splits also even
+// out the last wave (924 queries over 57,600 keys, 24 heads, 96 CTAs: 900 us alone, 785 in three
+// splits), if they gain a tenth by this count: the waves read K and V again (1,200 queries, 120
+// CTAs: 1,012 us alone, 1,088 in six); fp32 runs four that share it, and splits only fill the first.
+// Against "at least two tiles a split (fp32: four), at most 16, within one wave": 1 query over
+// 2,148 keys, 1 head 12.9 -> 10.5 us, over 30,000 37 -> 25; 300 queries over themselves, 24 heads:
+// no splits either way.
 int masked_splits(int n_q, int n_kv, int heads, int kv_heads, int head_dim, int dtype) {
   const bool tc = dtype == SFM_DTYPE_BF16;
   const long long ctas = tc ? base_ctas(n_q, heads, kv_heads) : (long long)((n_q + FM - 1) / FM) * heads;
   const int tiles = tc ? (n_kv + BKV - 1) / BKV : (n_kv + FN - 1) / FN;
-  const long long room = (tc ? kSms : 4 * kSms) / ctas;
-  const int most = (int)(room < kMaxKeySplits ? room : kMaxKeySplits);
-  const double tile = tc ? 2.0 : 3.4, part = 8e-6 / 4.0 * (head_dim + 1.0) * n_q * heads;
-  double best = tile * tiles;
+  const int most = tiles < kMaxKeySplits ? tiles : kMaxKeySplits;
+  const double tile = tc ? 2.0 : 3.4, cta = tc ? 7.0 : 0.0, part = 8e-6 / 4.0 * (head_dim + 1.0) * n_q * heads;
+  double best = 0.;
+  long long best_waves = 0;
   int splits = 1;
-  for (int s = 2; s <= most && s <= tiles; ++s) {
-    const double cost = tile * ((tiles + s - 1) / s) + 3.5 + part * s;
-    if (cost < best) {
+  for (int s = 1; s <= most; ++s) {
+    if (!tc && s > 1 && ctas * s > 4 * kSms) break;
+    const long long waves = tc ? (ctas * s + kSms - 1) / kSms : 1;
+    const double cost = waves * (tile * ((tiles + s - 1) / s) + cta) + (s > 1 ? 3.5 + part * s : 0.);
+    if (s == 1 || cost < (waves > best_waves ? 0.9 : 1.) * best) {
       best = cost;
+      best_waves = waves;
       splits = s;
     }
   }

@@ -208,6 +208,22 @@ def test_key_splits_join(cuda_device, dtype, d, n_q, n_kv, h, hk):
     run(q, k, v, lo, hi)
 
 
+@pytest.mark.parametrize("n_q,n_kv,h,hk", [(924, 9000, 24, 8), (1848, 17000, 24, 24)])
+def test_key_splits_over_several_waves(cuda_device, n_q, n_kv, h, hk):
+    # more CTAs than SMs, and keys split all the same
+    from streaming_flow_matching_b200 import attention_bounds, attention_masked
+    need = L.lib.sfm_attention_masked_workspace_bytes(n_q, n_kv, h, hk, 128, L.SFM_DTYPE_BF16)
+    splits = need // (n_q * h * 129 * 4)
+    assert splits > 1 and splits * h * (n_q // 256) > 148
+    q, k, v = make(n_q, n_kv, h, hk, 128, BF, seed=3)
+    lo, hi = attention_bounds(n_q, n_kv, causal=True)
+    out = attention_masked(q, k, v, lo, hi)
+    assert L.check_call_error() == 0
+    at = torch.cat([torch.arange(0, n_q, 97, device="cuda"), ints([n_q - 1]).long()])
+    ref, mag, _ = R.attend(q[at], k, v, lo[at], hi[at])
+    check(out[at], ref, mag, BF)
+
+
 @pytest.mark.parametrize("h,hk", [(16, 16), (16, 8)])
 def test_more_blocks_than_sms(cuda_device, h, hk):
     # several waves of query blocks: all keys, few, none
