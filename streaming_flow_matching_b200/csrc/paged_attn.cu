@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int NO = NV >= 8 ? NV / 8 : 1;                     // of them a lane's own: v0, ... of one head,
   constexpr int DUP = NV >= 8 ? 1 : 8 / NV;                    // held by that many lanes
   constexpr int LPH = 8 / GT;                                  // lanes (of 8) of a head
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   float4* qs = reinterpret_cast<float4*>(smem + kWarps * Ring::kBytes);    // [GT][D / 4]
   float* obuf = reinterpret_cast<float*>(qs + GT * (D / 4));               // [kWarps][GT][D]
   float* mlbuf = obuf + kWarps * GT * D;                                   // [kWarps][GT][2]
@@ -820,19 +820,20 @@ __device__ void join_ml(const Split& sp, int G, int h, const Parts& p, int lane,
 }
 
 constexpr int kFinThreads = 256, kAccTok = 1024;
-constexpr int kTokThread = kAccTok / kFinThreads, kHeadsOnce = 4;
+constexpr int kTokThread = kAccTok / kFinThreads, kHeadsOnce = 4, kSumsOnce = 32;
 
 // The finishing kernel.  Its first CTAs join, one per (sequence, query head): a sequence
 // finished by one CTA is left alone, an empty one gets zeros; the partials are summed in a
 // fixed order (float4 column x run, runs strided over the CTA, then over its groups).  The
 // others add weights, one per (sequence, key head, kAccTok slots): weights += sum over the
 // key head's query heads of 2^(score - lse).  Only the part that does not depend on the
-// attention kernel runs before the wait for it.
+// attention kernel runs before the wait for it.  (80 registers; 64 spill and are 2 to 15 % slower
+// with weights, a kernel of 47 for the joins alone 2 to 5 % where few sequences are joined.)
 template <typename T>
 __global__ void __launch_bounds__(kFinThreads)
     paged_finish_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp, int blocks_per_item) {
   __shared__ float4 buf[kFinThreads];
-  __shared__ float sh[kHeadsOnce];
+  __shared__ float sh[kSumsOnce];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.heads / a.c.kv_heads;
   if ((int)blockIdx.x < sp.joins) {
@@ -895,7 +896,8 @@ __global__ void __launch_bounds__(kFinThreads)
 #pragma unroll
   for (int i = 0; i < kTokThread; ++i) step[i] = 0.f;
   for (int g0 = 0; g0 < G; g0 += kHeadsOnce) {
-    // the scores of a few heads are on their way while their log-sum-exps are made, a warp each
+    // the scores of a few heads are on their way while the log-sum-exps of up to kSumsOnce are
+    // made, a warp each
     float s[kHeadsOnce][kTokThread];
 #pragma unroll
     for (int x = 0; x < kHeadsOnce; ++x)
@@ -904,26 +906,28 @@ __global__ void __launch_bounds__(kFinThreads)
         const int t = blk * kAccTok + i * kFinThreads + tid;
         s[x][i] = g0 + x < G && t < t1 ? __ldcg(sc + (size_t)(g0 + x) * sp.pitch + i * kFinThreads) : -INFINITY;
       }
-    if (warp < kHeadsOnce && g0 + warp < G) {
-      const int h = hk * G + g0 + warp;
-      float m, l;
-      if (p.s0 == p.s1) {                                      // the attention kernel left it whole
-        m = __ldcg(sp.lse + (size_t)seq * a.heads + h);
-      } else {
-        join_ml(sp, G, h, p, lane, &m, &l);
-        m += log2f(l);
+    if (g0 % kSumsOnce == 0) {
+      if (g0) __syncthreads();
+      for (int x = warp; x < kSumsOnce && g0 + x < G; x += kFinThreads / 32) {
+        const int h = hk * G + g0 + x;
+        float m, l;
+        if (p.s0 == p.s1) {                                    // the attention kernel left it whole
+          m = __ldcg(sp.lse + (size_t)seq * a.heads + h);
+        } else {
+          join_ml(sp, G, h, p, lane, &m, &l);
+          m += log2f(l);
+        }
+        if (lane == 0) sh[x] = m;
       }
-      if (lane == 0) sh[warp] = m;
+      __syncthreads();
     }
-    __syncthreads();
 #pragma unroll
     for (int x = 0; x < kHeadsOnce; ++x) {
-      const float ls = g0 + x < G ? sh[x] : -INFINITY;
+      const float ls = g0 + x < G ? sh[g0 % kSumsOnce + x] : -INFINITY;
       if (ls == -INFINITY) continue;                           // no visible slot (every page bad)
 #pragma unroll
       for (int i = 0; i < kTokThread; ++i) step[i] += ex2_approx(s[x][i] - ls);
     }
-    __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < kTokThread; ++i) {
@@ -1028,9 +1032,8 @@ int launch_paged_attention(const DecodeArgs& a, int dtype, void* workspace, cuda
   ProfScope ps(SFM_PROF_ATTN_MERGE, s);
   const int per_item = (a.c.max_tokens + kAccTok - 1) / kAccTok;
   const unsigned fin = (unsigned)(sp.joins + (a.weights ? a.c.n_seq * a.c.kv_heads * per_item : 0));
-  if (dtype == SFM_DTYPE_BF16)
-    return record_cuda(launch_dependent(paged_finish_kernel<__nv_bfloat16>, fin, kFinThreads, 0, s, a, sp, per_item));
-  return record_cuda(launch_dependent(paged_finish_kernel<float>, fin, kFinThreads, 0, s, a, sp, per_item));
+  auto kernel = dtype == SFM_DTYPE_BF16 ? paged_finish_kernel<__nv_bfloat16> : paged_finish_kernel<float>;
+  return record_cuda(launch_dependent(kernel, fin, kFinThreads, 0, s, a, sp, per_item));
 }
 
 }  // namespace sfm
