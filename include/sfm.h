@@ -503,7 +503,8 @@ SFM_API int sfm_paged_append(const void* k, const void* v, void* k_pages, void* 
  * go together; without slopes they are not read.  Any number of query heads per key
  * head.  Results do not depend on timing (partials are joined in a fixed order).
  * workspace: the size for max_tokens = max_pages * page_size, or cap where that is
- * smaller and the call has state arrays.
+ * smaller and the call has state arrays (may be NULL when it is 0: small batches of
+ * short sequences need none, so a table no wider than needed pays).
  */
 SFM_API size_t sfm_paged_attention_workspace_bytes(int n_seq, int max_tokens, int n_heads,
                                                    int n_kv_heads, int head_dim, int dtype,

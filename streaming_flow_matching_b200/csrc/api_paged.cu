@@ -123,7 +123,7 @@ int sfm_paged_attention(const void* q, const void* k_pages, const void* v_pages,
     return SFM_EUNSUPPORTED;
   const size_t need =
       paged_attention_workspace(n_seq, a.c.max_tokens, n_heads, n_kv_heads, head_dim, dtype, weights != nullptr);
-  if (workspace_bytes < need || !workspace || !aligned(workspace, 16)) return SFM_EINVAL;
+  if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 16)))) return SFM_EINVAL;
   Guard gd;
   if ((rc = call_guard(&gd))) return rc;
   a.q = q;

@@ -188,6 +188,14 @@ def test_attention_lengths_and_heads(cuda_device, dtype, d, page, h, hk):
     assert int(torch.count_nonzero(out[1])) == 0 and int(torch.count_nonzero(out[5])) == 0
     w = torch.rand(len(lens), hk, 310, device="cuda")
     run(c, q, lens, softcap=20.0, slopes=ladder(h), weights=w)
+    # a table for far longer sequences: the form of long ones (a workspace, a second kernel)
+    c.table = torch.cat([c.table, torch.full((len(lens), 40000 // page), -1, dtype=torch.int32, device="cuda")], 1)
+    need = L.lib.sfm_paged_attention_workspace_bytes
+    code = L.SFM_DTYPE_BF16 if dtype == BF else L.SFM_DTYPE_FP32
+    assert need(len(lens), c.table.shape[1] * page, h, hk, d, code, 0) > 0
+    out = run(c, q, lens)
+    assert int(torch.count_nonzero(out[1])) == 0 and int(torch.count_nonzero(out[5])) == 0
+    run(c, q, lens, softcap=20.0, slopes=ladder(h), weights=torch.rand(len(lens), hk, 40000, device="cuda"))
 
 
 @pytest.mark.parametrize("dtype,d,h,hk,lens", [
@@ -231,6 +239,28 @@ def test_positions_without_a_bias_change_nothing(cuda_device, dtype, d):
     w = torch.zeros(3, 2, 300, device="cuda")
     a = paged_attention(q, c.k, c.v, c.table, ints(lens), positions=pos, q_positions=ints([9999] * 3), weights=w)
     assert torch.equal(a, run(c, q, lens, weights=torch.zeros_like(w)))
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 32), (F32, 128)])
+@pytest.mark.parametrize("h,hk,lens", [
+    (2, 1, [60, 64, 1]), (2, 1, [128, 65, 3]), (8, 2, [256, 1, 0, 129]), (4, 1, [512, 449, 70]), (16, 1, [1000]),
+    (3, 3, [1500, 900]), (40, 1, [700, 500]), (5, 5, [1024] * 4)])
+def test_attention_clusters(cuda_device, dtype, d, h, hk, lens):
+    # one kernel for short sequences: 1, 2, 4 and 8 CTAs a sequence, some without a tile
+    from streaming_flow_matching_b200 import paged_attention
+    need = L.lib.sfm_paged_attention_workspace_bytes
+    code = L.SFM_DTYPE_BF16 if dtype == BF else L.SFM_DTYPE_FP32
+    c = Cache(lens, 16, hk, d, dtype, seed=h)
+    assert h * hk == 40 or need(len(lens), c.table.shape[1] * 16, h, hk, d, code, 0) == 0
+    q = (torch.randn(len(lens), h, d, device="cuda") * 1.5).to(dtype)
+    w = torch.rand(len(lens), hk, max(lens), device="cuda")
+    kw = dict(softcap=30.0, slopes=ladder(h))
+    a = run(c, q, lens, **kw)
+    run(c, q, lens, weights=w, **kw)
+    assert torch.equal(a, run(c, q, lens, **kw))             # the same bits
+    c.v.view(-1, hk, d)[c.rows(0, lens[0])[-1]] = float("inf")   # an infinity reaches its sequence's heads
+    out = paged_attention(q, c.k, c.v, c.table, ints(lens))
+    assert bool((out[0] == float("inf")).all()) and bool(torch.isfinite(out[1:]).all())
 
 
 def test_attention_many_sequences(cuda_device):
@@ -616,7 +646,7 @@ def test_refusals(cuda_device):
         (lambda: paged_attention(q, c.k, c.v, c.table, lens, q_positions=lens), L.SfmError),
         (lambda: paged_attention(q, c.k, c.v, c.table, lens, weights=w[:, :1].contiguous()), ValueError),
         (lambda: paged_attention(q, c.k, c.v, c.table, lens, weights=w.double()), ValueError),
-        (lambda: paged_attention(q, c.k, c.v, c.table, lens,
+        (lambda: paged_attention(q, c.k, c.v, c.table.repeat(1, 400), lens,      # a long table needs more
                                  workspace=torch.empty(64, dtype=torch.uint8, device="cuda")), L.SfmError),
         (lambda: paged_append(k, k, c.k, c.v, c.table, lens, row_starts=ints([0, 2])), ValueError),
         (lambda: paged_append(torch.cat([k, k]), torch.cat([k, k]), c.k, c.v, c.table, lens), L.SfmError),

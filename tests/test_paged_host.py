@@ -19,8 +19,8 @@ def append(**kw):
 
 
 def attention(**kw):
-    a = dict(q=P, kp=P, vp=P, table=P, lengths=P, o=2 * P, n_seq=2, n_pages=8, page=16, width=4, h=4, hk=2, d=128,
-             dtype=BF, cap=0.0, slopes=P, positions=P, q_positions=P, weights=P, room=64, ws=P, ws_bytes=1 << 40)
+    a = dict(q=P, kp=P, vp=P, table=P, lengths=P, o=2 * P, n_seq=2, n_pages=8, page=16, width=1024, h=4, hk=2,
+             d=128, dtype=BF, cap=0.0, slopes=P, positions=P, q_positions=P, weights=P, room=1 << 14, ws=P, ws_bytes=1 << 40)
     a.update(kw)
     return L.lib.sfm_paged_attention(*a.values(), None)
 
@@ -120,11 +120,15 @@ def test_sizes_past_what_32_bits_index():
 
 def test_workspaces():
     att = L.lib.sfm_paged_attention_workspace_bytes
-    assert att(4, 1000, 24, 8, 128, BF, 0) % 16 == 0
+    assert att(4, 9000, 24, 8, 128, BF, 0) % 16 == 0
     # the raw scores of every slot and query head, when weights are accumulated
-    assert att(4, 1000, 24, 8, 128, BF, 1) - att(4, 1000, 24, 8, 128, BF, 0) == 4 * 24 * 1000 * 4 + 4 * 24 * 4
+    assert att(4, 9000, 24, 8, 128, BF, 1) - att(4, 9000, 24, 8, 128, BF, 0) == 4 * 24 * 9000 * 4 + 4 * 24 * 4
     # without them it does not depend on the lengths
-    assert att(4, 10, 24, 8, 128, BF, 0) == att(400, 100000, 24, 8, 128, BF, 0)
+    assert att(4, 9000, 24, 8, 128, BF, 0) == att(400, 100000, 24, 8, 128, BF, 0)
+    # small batches of short sequences need none, as long as one head group adds to the weights
+    assert att(3, 1300, 24, 8, 128, BF, 0) == att(2, 300, 24, 8, 128, BF, 1) == att(2, 60, 8, 2, 64, F32, 1) == 0
+    assert att(1, 100, 40, 1, 128, BF, 0) == 0 and att(1, 100, 40, 1, 128, BF, 1) > 0
+    assert att(300, 100, 2, 1, 128, BF, 0) > 0
     for bad in ((0, 10, 4, 2, 128, BF, 0), (1, 0, 4, 2, 128, BF, 0), (1, 10, 4, 3, 128, BF, 0),
                 (1, 10, 4, 2, 64, BF, 0), (1, 10, 4, 2, 128, 9, 0)):
         assert att(*bad) == 0
