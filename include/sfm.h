@@ -526,7 +526,7 @@ SFM_API int sfm_paged_attention(const void* q, const void* k_pages, const void* 
  * what they held.  lengths is not changed (each layer cuts at the same lengths);
  * the new one is min(lengths[s], keep), and pages behind it are free.
  * SFM_EINVAL if keep < 1 or n_first + n_recent > keep.  workspace: max_tokens as for
- * sfm_paged_attention, cap included.
+ * sfm_paged_attention, cap included (may be NULL when it is 0).
  */
 SFM_API size_t sfm_paged_evict_workspace_bytes(int n_seq, int max_tokens, int n_kv_heads, int keep);
 SFM_API int sfm_paged_evict(void* k_pages, void* v_pages, const int* table, const int* lengths,

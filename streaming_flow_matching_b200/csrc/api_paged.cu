@@ -161,7 +161,7 @@ int sfm_paged_evict(void* k_pages, void* v_pages, const int* table, const int* l
   if (rc) return rc;
   if (!fits_grid((long long)n_seq * n_kv_heads * 4096)) return SFM_EUNSUPPORTED;
   const size_t need = paged_evict_workspace(n_seq, a.c.max_tokens, n_kv_heads, keep);
-  if (workspace_bytes < need || !workspace || !aligned(workspace, 16)) return SFM_EINVAL;
+  if (workspace_bytes < need || (need && (!workspace || !aligned(workspace, 16)))) return SFM_EINVAL;
   Guard gd;
   if ((rc = call_guard(&gd))) return rc;
   a.k_pages = k_pages;

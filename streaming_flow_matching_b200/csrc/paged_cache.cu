@@ -123,6 +123,51 @@ __device__ __forceinline__ int warp_sum(int v) {
 // The ranks are made once and kept in shared memory (`held` of them at most; a longer run of
 // slots makes them again in each of its passes).  Bound by instructions: a CTA passes over its
 // slots five times, so those passes over shared memory are kept short.
+// A warp moves kMoveRows rows at a time: their slots and pages are looked up by as many
+// lanes at once, then the 16-byte pieces of all of them (head_vecs of K and of V each) are
+// loaded four to a lane before the first is stored.
+constexpr int kMoveWarps = 8, kMoveRows = 8;
+
+// Warp `warp` of `warps` moves its share of an item's n rows.
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int item, const int* outs, const int* mvs, int n,
+                                          int warp, int warps, int head_vecs) {
+  const int seq = item / a.c.kv_heads, h = item - seq * a.c.kv_heads;
+  const int lane = threadIdx.x & 31;
+  const int pieces = 2 * head_vecs;                            // of a row; kMoveRows * pieces is a multiple of 128
+  uint4* kp = reinterpret_cast<uint4*>(a.k_pages);
+  uint4* vp = reinterpret_cast<uint4*>(a.v_pages);
+  for (int i0 = warp * kMoveRows; i0 < n; i0 += warps * kMoveRows) {
+    int rt = -1, rf = -1;
+    if (lane < kMoveRows && i0 + lane < n) {
+      const int to = outs[i0 + lane], from = mvs[i0 + lane];
+      rt = cache_row(a.c, seq, to, a.err);
+      rf = cache_row(a.c, seq, from, a.err);
+      const size_t at = (size_t)item * a.cap;
+      a.weights[at + to] = a.weights[at + from];
+      a.positions[at + to] = a.positions[at + from];
+    }
+    for (int x0 = lane; x0 < kMoveRows * pieces; x0 += 128) {
+      uint4 d[4];
+      uint4* to[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int x = x0 + 32 * u, r = x / pieces, c = x - r * pieces;
+        const int from_row = __shfl_sync(0xffffffffu, rf, r), to_row = __shfl_sync(0xffffffffu, rt, r);
+        uint4* pool = c < head_vecs ? kp : vp;
+        const int cc = c < head_vecs ? c : c - head_vecs;
+        to[u] = nullptr;
+        if (from_row >= 0 && to_row >= 0) {
+          d[u] = pool[((size_t)from_row * a.c.kv_heads + h) * head_vecs + cc];
+          to[u] = pool + ((size_t)to_row * a.c.kv_heads + h) * head_vecs + cc;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (to[u]) *to[u] = d[u];
+    }
+  }
+}
+
 // slots of each CTA of a cluster, whole warps of them
 __host__ __device__ inline int select_run(int n, int parts) { return ((n + parts - 1) / parts + 31) & ~31; }
 
@@ -161,7 +206,7 @@ __device__ __forceinline__ uint2 peer_words(const void* p, int rank) {          
 template <bool HOLD>
 __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict__ counts, int* __restrict__ lists,
                                              int room, int item, int part_id, int parts, int from, int n,
-                                             SelectShared& sh) {
+                                             int fused_vecs, SelectShared& sh) {
   extern __shared__ unsigned ranks[];
   auto& part = sh.part;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -314,7 +359,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
     no += warp_sum(lane < part_id ? (int)peer_word(&sh.total[2], lane) : 0);
     nm += warp_sum(lane < part_id ? (int)peer_word(&sh.total[3], lane) : 0);
   }
-  int* outs = lists + (size_t)item * 2 * room;
+  int* outs = fused_vecs ? reinterpret_cast<int*>(sh.hist) : lists + (size_t)item * 2 * room;
   int* mvs = outs + room;
   const unsigned lower = (1u << lane) - 1u;
   int tie = tie_base;
@@ -346,6 +391,11 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
   };
   walk(t0, mid, false, outs, no);
   nm = walk(mid, t1, true, mvs, nm);
+  if (fused_vecs) {                                            // a CTA that is alone, and few rows
+    __syncthreads();
+    move_rows(a, item, outs, mvs, warp_sum(part[2][lane]), warp, kSelWarps, fused_vecs);
+    return;
+  }
   // as many slots were evicted before `keep` as are kept behind it
   if (part_id == parts - 1 && warp == kSelWarps - 1 && lane == 0) counts[item] = nm;
   if (parts > 1) cluster_barrier(parts);                       // nobody leaves while its words are read
@@ -353,69 +403,28 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
 
 __global__ void __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictArgs a, int* __restrict__ counts,
-                        int* __restrict__ lists, int room, int held, int parts) {
+                        int* __restrict__ lists, int room, int held, int parts, int fused_vecs) {
   __shared__ SelectShared sh;
   grid_dependency_wait();
   const int item = blockIdx.x / parts, part_id = blockIdx.x - item * parts;
   const int n = cache_len(a.c, item / a.c.kv_heads, a.err);
   if (n <= a.keep) {                                           // the same for the whole cluster
-    if (threadIdx.x == 0 && part_id == 0) counts[item] = 0;
+    if (threadIdx.x == 0 && part_id == 0 && !fused_vecs) counts[item] = 0;
     return;
   }
   const int run = select_run(n, parts), from = min(n, part_id * run), mine = min(n - from, run);
-  if (run <= held) evict_select<true>(a, counts, lists, room, item, part_id, parts, from, mine, sh);
-  else evict_select<false>(a, counts, lists, room, item, part_id, parts, from, mine, sh);
+  if (run <= held) evict_select<true>(a, counts, lists, room, item, part_id, parts, from, mine, fused_vecs, sh);
+  else evict_select<false>(a, counts, lists, room, item, part_id, parts, from, mine, fused_vecs, sh);
 }
-
-// A warp moves kMoveRows rows at a time: their slots and pages are looked up by as many
-// lanes at once, then the 16-byte pieces of all of them (head_vecs of K and of V each) are
-// loaded four to a lane before the first is stored.
-constexpr int kMoveWarps = 8, kMoveRows = 8;
 
 __global__ void __launch_bounds__(kMoveWarps * 32)
     evict_move_kernel(const __grid_constant__ EvictArgs a, const int* __restrict__ counts,
                       const int* __restrict__ lists, int room, int head_vecs, int blocks_per_item) {
   grid_dependency_wait();
   const int item = blockIdx.x / blocks_per_item, blk = blockIdx.x - item * blocks_per_item;
-  const int seq = item / a.c.kv_heads, h = item - seq * a.c.kv_heads;
-  const int lane = threadIdx.x & 31;
-  const int n = counts[item];
   const int* outs = lists + (size_t)item * 2 * room;
-  const int* mvs = outs + room;
-  const int pieces = 2 * head_vecs;                            // of a row; kMoveRows * pieces is a multiple of 128
-  uint4* kp = reinterpret_cast<uint4*>(a.k_pages);
-  uint4* vp = reinterpret_cast<uint4*>(a.v_pages);
-  for (int i0 = (blk * kMoveWarps + (threadIdx.x >> 5)) * kMoveRows; i0 < n;
-       i0 += blocks_per_item * kMoveWarps * kMoveRows) {
-    int rt = -1, rf = -1;
-    if (lane < kMoveRows && i0 + lane < n) {
-      const int to = outs[i0 + lane], from = mvs[i0 + lane];
-      rt = cache_row(a.c, seq, to, a.err);
-      rf = cache_row(a.c, seq, from, a.err);
-      const size_t at = (size_t)item * a.cap;
-      a.weights[at + to] = a.weights[at + from];
-      a.positions[at + to] = a.positions[at + from];
-    }
-    for (int x0 = lane; x0 < kMoveRows * pieces; x0 += 128) {
-      uint4 d[4];
-      uint4* to[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int x = x0 + 32 * u, r = x / pieces, c = x - r * pieces;
-        const int from_row = __shfl_sync(0xffffffffu, rf, r), to_row = __shfl_sync(0xffffffffu, rt, r);
-        uint4* pool = c < head_vecs ? kp : vp;
-        const int cc = c < head_vecs ? c : c - head_vecs;
-        to[u] = nullptr;
-        if (from_row >= 0 && to_row >= 0) {
-          d[u] = pool[((size_t)from_row * a.c.kv_heads + h) * head_vecs + cc];
-          to[u] = pool + ((size_t)to_row * a.c.kv_heads + h) * head_vecs + cc;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (to[u]) *to[u] = d[u];
-    }
-  }
+  move_rows(a, item, outs, outs + room, counts[item], blk * kMoveWarps + (threadIdx.x >> 5),
+            blocks_per_item * kMoveWarps, head_vecs);
 }
 
 }  // namespace
@@ -437,8 +446,31 @@ static int evict_room(int max_tokens, int keep) {
   return past <= 0 ? 0 : past < keep ? past : keep;
 }
 
+// CTAs per item: a slot costs one CTA 0.6 ns, a cluster of 2, 4 or 8 costs 3.6, 6.3 and some 9 us
+// for its barriers and histograms, and clusters fill about 128 SMs: two or four where a CTA has
+// more than 12K slots (8 heads of 30,000: 27.8 us alone, 23.7, 22.6, and with eight 23.7; of
+// 8,000: 14.6, 17.9, 19.6, 22.2), and as many as hold the ranks (24 heads of 57,600 in passes
+// over global memory 101 us, held by four 30.8).
+static int evict_parts(long long items, int max_tokens) {
+  int parts = 1;
+  while (parts < 4 && items * parts * 2 <= 128 && max_tokens / parts > 12 * 1024) parts *= 2;
+  while (parts < 8 && select_run(max_tokens, parts) > kHeldRanks) parts *= 2;
+  return parts;
+}
+// So few rows that the CTA that ranks an item moves them too: its lists stay in shared memory, and
+// neither a workspace nor a second launch is needed.  The host's time is 14.8 -> 9.9 us; on the
+// device, all rows moved, 8 items of 100 to 50: 11.8 -> 10.3 us, 32 of 1,200 to 924: 14.2 -> 15.8,
+// 8 of 1,024 to 512: 13.1 -> 17.8 (one SM moves what all could), but 128 of them 20.3 -> 18.4; 384
+// (several waves) 48 -> 53 with few moves.
+constexpr int kFusedRows = 512, kFusedRowsFew = 320;
+static bool evict_fused(long long items, int max_tokens, int keep) {
+  const int rows = items > kSms ? 0 : items >= 64 ? kFusedRows : kFusedRowsFew;
+  return evict_room(max_tokens, keep) <= rows && evict_parts(items, max_tokens) == 1;
+}
+
 size_t paged_evict_workspace(int n_seq, int max_tokens, int kv_heads, int keep) {
   const size_t items = (size_t)n_seq * kv_heads;
+  if (evict_fused((long long)items, max_tokens, keep)) return 0;
   const size_t b = (items + items * 2 * evict_room(max_tokens, keep)) * sizeof(int);
   return (b + 15) / 16 * 16;
 }
@@ -450,21 +482,16 @@ int launch_paged_evict(const EvictArgs& a, int row_bytes_head, void* workspace, 
   int* counts = (int*)workspace;
   int* lists = counts + items;
   ProfScope ps(SFM_PROF_APPEND, s);
-  // CTAs per item: a slot costs one CTA 0.6 ns, a cluster of 2, 4 or 8 costs 3.6, 6.3 and some 9 us
-  // for its barriers and histograms, and clusters fill about 128 SMs: two or four where a CTA has
-  // more than 12K slots (8 heads of 30,000: 27.8 us alone, 23.7, 22.6, and with eight 23.7; of
-  // 8,000: 14.6, 17.9, 19.6, 22.2), and as many as hold the ranks (24 heads of 57,600 in passes
-  // over global memory 101 us, held by four 30.8).
-  int parts = 1;
-  while (parts < 4 && (long long)items * parts * 2 <= 128 && a.c.max_tokens / parts > 12 * 1024) parts *= 2;
-  while (parts < 8 && select_run(a.c.max_tokens, parts) > kHeldRanks) parts *= 2;
+  const int parts = evict_parts(items, a.c.max_tokens);
+  const bool fused = evict_fused(items, a.c.max_tokens, a.keep);
   const int run = select_run(a.c.max_tokens, parts), held = run < kHeldRanks ? run : kHeldRanks;
   const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kHeldRanks * (int)sizeof(unsigned));
   if (e != cudaSuccess) return record_cuda(e);
   int rc = record_cuda(launch_dependent_clusters(evict_select_kernel, parts, (unsigned)(items * parts), kSelThreads,
-                                                 held * sizeof(unsigned), s, a, counts, lists, room, held, parts));
-  if (rc) return rc;
+                                                 held * sizeof(unsigned), s, a, counts, lists, room, held, parts,
+                                                 fused ? row_bytes_head / 16 : 0));
+  if (rc || fused) return rc;
   // kMoveRows rows per warp, and no more CTAs than fill the device several times over
   int blocks = (room + kMoveRows * kMoveWarps - 1) / (kMoveRows * kMoveWarps);
   const int most = (kSms * 32 + items - 1) / items;

@@ -514,6 +514,19 @@ def test_evict_in_clusters(cuda_device, hk, lens, cap, keep, kind):
     evict_case(c, lens, w, pos.view(len(lens), hk, cap).to(torch.int32), keep, 3, keep // 4)
 
 
+@pytest.mark.parametrize("n_seq,hk,n,keep,alone", [
+    (9, 8, 1024, 512, True), (20, 8, 300, 150, False), (2, 2, 640, 320, True), (2, 2, 650, 325, False),
+    (3, 1, 7000, 6700, True)])
+def test_evict_many_rows_in_one_kernel_or_two(cuda_device, n_seq, hk, n, keep, alone):
+    assert (L.lib.sfm_paged_evict_workspace_bytes(n_seq, n, hk, keep) == 0) == alone
+    lens = [n - 3 * s for s in range(n_seq)]
+    for w in (torch.arange(n, device="cuda").expand(n_seq, hk, n).float().contiguous(),     # all that can move
+              torch.rand(n_seq, hk, n, device="cuda")):
+        c = Cache(lens, 16, hk, 128, BF, seed=6)
+        pos = torch.arange(n, device="cuda", dtype=torch.int32).expand(n_seq, hk, n).contiguous()
+        evict_case(c, lens, w, pos, keep, 0, 1)
+
+
 def test_evict_more_than_clusters_hold(cuda_device):
     n = 400000                                               # 8 CTAs hold 393,216 ranks
     c = Cache([n], 512, 1, 32, F32, seed=5)

@@ -26,8 +26,8 @@ def attention(**kw):
 
 
 def evict(**kw):
-    a = dict(kp=P, vp=P, table=P, lengths=P, weights=P, positions=P, room=64, n_seq=2, n_pages=8, page=16, width=4,
-             hk=2, d=128, dtype=BF, keep=8, first=0, recent=0, ws=P, ws_bytes=1 << 40)
+    a = dict(kp=P, vp=P, table=P, lengths=P, weights=P, positions=P, room=9000, n_seq=2, n_pages=8, page=16, width=600,
+             hk=2, d=128, dtype=BF, keep=8000, first=0, recent=0, ws=P, ws_bytes=1 << 40)
     a.update(kw)
     return L.lib.sfm_paged_evict(*a.values(), None)
 
@@ -74,7 +74,7 @@ def test_attention_arguments(bad):
     assert attention(**bad) == L.SFM_EINVAL
 
 
-@pytest.mark.parametrize("bad", [dict(keep=0), dict(first=-1), dict(recent=-1), dict(first=5, recent=4),
+@pytest.mark.parametrize("bad", [dict(keep=0), dict(first=-1), dict(recent=-1), dict(keep=8, first=5, recent=4),
                                  dict(first=2 ** 31 - 1, recent=2 ** 31 - 1), dict(weights=None),
                                  dict(positions=None), dict(room=0), dict(ws=None), dict(ws_bytes=0)])
 def test_evict_arguments(bad):
@@ -133,7 +133,8 @@ def test_workspaces():
                 (1, 10, 4, 2, 64, BF, 0), (1, 10, 4, 2, 128, 9, 0)):
         assert att(*bad) == 0
     ev = L.lib.sfm_paged_evict_workspace_bytes
-    assert ev(2, 100, 4, 90) == (8 + 8 * 2 * 10) * 4 and ev(2, 100, 4, 100) >= 8 * 4
+    assert ev(2, 9000, 4, 8000) == (8 + 8 * 2 * 1000) * 4
+    assert ev(2, 100, 4, 90) == ev(2, 100, 4, 100) == ev(16, 9000, 8, 8500) == 0      # few rows to move: none
     assert ev(0, 100, 4, 90) == 0 and ev(2, 100, 4, 0) == 0
     mk = L.lib.sfm_attention_masked_workspace_bytes
     assert mk(4096, 4096, 24, 8, 128, BF) == 0                # enough query blocks: no splits
