@@ -1192,8 +1192,8 @@ long long base_ctas(int n_q, int heads, int kv_heads) {
 }  // namespace
 
 // Key splits, as many as cost least: a split's key tiles of the longest possible range (2 us each,
-// fp32 3.4) and, bf16, a CTA's set-up and output (7 us), in every wave of CTAs; the join (3.5 us)
-// and the partials (written and read, 4 TB/s).  bf16 runs one CTA on an SM, so that splits also even
+// fp32 3.4) and, bf16, a CTA's set-up and output (7 us), in every wave of CTAs; the join (3.5 us,
+// and 2.5 of its 4 us of the host's time) and the partials (written and read, 4 TB/s).  bf16 runs one CTA on an SM, so that splits also even
 // out the last wave (924 queries over 57,600 keys, 24 heads, 96 CTAs: 900 us alone, 785 in three
 // splits), if they gain a tenth by this count: the waves read K and V again (1,200 queries, 120
 // CTAs: 1,012 us alone, 1,088 in six); fp32 runs four that share it, and splits only fill the first.
@@ -1212,7 +1212,7 @@ int masked_splits(int n_q, int n_kv, int heads, int kv_heads, int head_dim, int 
   for (int s = 1; s <= most; ++s) {
     if (!tc && s > 1 && ctas * s > 4 * kSms) break;
     const long long waves = tc ? (ctas * s + kSms - 1) / kSms : 1;
-    const double cost = waves * (tile * ((tiles + s - 1) / s) + cta) + (s > 1 ? 3.5 + part * s : 0.);
+    const double cost = waves * (tile * ((tiles + s - 1) / s) + cta) + (s > 1 ? 6. + part * s : 0.);
     if (s == 1 || cost < (waves > best_waves ? 0.9 : 1.) * best) {
       best = cost;
       best_waves = waves;
