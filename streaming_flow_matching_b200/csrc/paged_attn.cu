@@ -1146,8 +1146,10 @@ cudaError_t launch_attn(K kernel, int smem, const DecodeArgs& a, const Split& sp
 template <int NT, bool CLUSTER>
 cudaError_t launch_bf16(const DecodeArgs& a, const Split& sp, cudaStream_t s) {
   const bool cap = a.softcap > 0.f, bias = a.slopes != nullptr;
-  auto kernel = cap ? (bias ? paged_attn_bf16_kernel<NT, true, true, CLUSTER> : paged_attn_bf16_kernel<NT, true, false, CLUSTER>)
-                    : (bias ? paged_attn_bf16_kernel<NT, false, true, CLUSTER> : paged_attn_bf16_kernel<NT, false, false, CLUSTER>);
+  auto kernel = cap && bias ? paged_attn_bf16_kernel<NT, true, true, CLUSTER>
+                : cap       ? paged_attn_bf16_kernel<NT, true, false, CLUSTER>
+                : bias      ? paged_attn_bf16_kernel<NT, false, true, CLUSTER>
+                            : paged_attn_bf16_kernel<NT, false, false, CLUSTER>;
   return launch_attn(kernel, kSmemBf16, a, sp, s);
 }
 
@@ -1160,7 +1162,8 @@ cudaError_t launch_fp32(const DecodeArgs& a, const Split& sp, cudaStream_t s) {
 
 template <bool CLUSTER>
 cudaError_t launch_any(const DecodeArgs& a, const Split& sp, int dtype, cudaStream_t s) {
-  if (dtype == SFM_DTYPE_BF16) return sp.hpt == 8 ? launch_bf16<1, CLUSTER>(a, sp, s) : launch_bf16<2, CLUSTER>(a, sp, s);
+  if (dtype == SFM_DTYPE_BF16)
+    return sp.hpt == 8 ? launch_bf16<1, CLUSTER>(a, sp, s) : launch_bf16<2, CLUSTER>(a, sp, s);
   switch (a.c.head_dim / 32) {
     case 1: return launch_fp32<1, CLUSTER>(a, sp, s);
     case 2: return launch_fp32<2, CLUSTER>(a, sp, s);

@@ -20,7 +20,8 @@ def append(**kw):
 
 def attention(**kw):
     a = dict(q=P, kp=P, vp=P, table=P, lengths=P, o=2 * P, n_seq=2, n_pages=8, page=16, width=1024, h=4, hk=2,
-             d=128, dtype=BF, cap=0.0, slopes=P, positions=P, q_positions=P, weights=P, room=1 << 14, ws=P, ws_bytes=1 << 40)
+             d=128, dtype=BF, cap=0.0, slopes=P, positions=P, q_positions=P, weights=P, room=1 << 14, ws=P,
+             ws_bytes=1 << 40)
     a.update(kw)
     return L.lib.sfm_paged_attention(*a.values(), None)
 
