@@ -845,6 +845,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 
   tc_fence_before();
+  __syncwarp();                                                // the roles' single lanes are back
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -1193,10 +1194,11 @@ long long base_ctas(int n_q, int heads, int kv_heads) {
 
 // Key splits, as many as cost least: a split's key tiles of the longest possible range (2 us each,
 // fp32 3.4) and, bf16, a CTA's set-up and output (7 us), in every wave of CTAs; the join (3.5 us,
-// and 2.5 of its 4 us of the host's time) and the partials (written and read, 4 TB/s).  bf16 runs one CTA on an SM, so that splits also even
-// out the last wave (924 queries over 57,600 keys, 24 heads, 96 CTAs: 900 us alone, 785 in three
-// splits), if they gain a tenth by this count: the waves read K and V again (1,200 queries, 120
-// CTAs: 1,012 us alone, 1,088 in six); fp32 runs four that share it, and splits only fill the first.
+// and 2.5 of its 4 us of the host's time) and the partials (written and read, 4 TB/s).  bf16 runs
+// one CTA on an SM, so that splits also even out the last wave (924 queries over 57,600 keys, 24
+// heads, 96 CTAs: 900 us alone, 785 in three splits), if they gain a tenth by this count: the waves
+// read K and V again (1,200 queries, 120 CTAs: 1,012 us alone, 1,088 in six); fp32 runs four that
+// share it, and splits only fill the first.
 // Against "at least two tiles a split (fp32: four), at most 16, within one wave": 1 query over
 // 2,148 keys, 1 head 12.9 -> 10.5 us, over 30,000 37 -> 25; 300 queries over themselves, 24 heads:
 // no splits either way.

@@ -152,6 +152,7 @@ __device__ __forceinline__ Share take_share(const DecodeArgs& a, const Split& sp
 
 // All threads of the cluster (or of the CTA that is alone); what they wrote to shared memory is seen.
 __device__ __forceinline__ void cluster_barrier(int parts) {
+  __syncwarp();                                                // (after loops of unequal length)
   if (parts == 1) __syncthreads();
   else sm100::cluster_sync();
 }
@@ -597,8 +598,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 // pieces that it fetched itself (no exchange, no bank conflicts).  The 8 lanes' sums of all
 // (head, step) scores are reduced and scattered in one go: with 4 heads and 4 steps 14 shuffles
 // leave each lane two scores, whose cap, bias and exponential are then done once and not by 8
-// lanes (with the deeper ring: 21 -> 11.4 us at the size above).  GT query heads per CTA (a larger group reads its keys again, from
-// L2).
+// lanes (with the deeper ring: 21 -> 11.4 us at the size above).  GT query heads per CTA (a
+// larger group reads its keys again, from L2).
 template <int DV>
 struct F32Ring {
   static constexpr int kSteps = DV == 4 ? 2 : 4, kTok = 4 * kSteps, kSub = kWarpTok / kTok;

@@ -181,6 +181,7 @@ struct __align__(8) SelectShared {
 
 // All threads of the cluster (or of the CTA that is alone); what they wrote to shared memory is seen.
 __device__ __forceinline__ void cluster_barrier(int parts) {
+  __syncwarp();                                                // (after loops of unequal length)
   if (parts == 1) __syncthreads();
   else sm100::cluster_sync();
 }
