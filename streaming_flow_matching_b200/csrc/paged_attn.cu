@@ -170,6 +170,7 @@ __device__ __forceinline__ float peer_float(const float* p, int rank) {
 // heads h0, ...; its scores of `count` slots from tok0 on, if weights are wanted, are
 // scores[head * held + slot - tok0].
 constexpr int kMaxParts = 8, kMaxTileHeads = 16;
+constexpr int kHeldTiles = 2;                                   // tiles a CTA of a cluster has at most, with weights
 template <typename T, int D>
 __device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Split& sp, int seq, int part, int h0, int nh,
                                                const float* part_o, float* part_ml, const float* scores, int tok0,
@@ -1106,7 +1107,7 @@ Plan make_plan(int n_seq, int max_tokens, int heads, int kv_heads, int head_dim,
   // 10.1 -> 8.9 us, with weights and 6 tiles 10.2 -> 12.4; 192 heads of 12 in 288 CTAs: 17.6 -> 28.3.
   const int max_tiles = (max_tokens + kTile - 1) / kTile;
   const long long items = (long long)n_seq * sp.hgroups;
-  const int most = weights ? 96 : 192, tiles = weights || sp.hpt == 16 ? 2 : 3;
+  const int most = weights ? 96 : 192, tiles = weights ? kHeldTiles : sp.hpt == 16 ? 2 : 3;
   int parts = 1;
   while (parts < kMaxParts && parts < max_tiles && items * parts * 2 <= most) parts *= 2;
   if (items * parts <= most && max_tiles <= tiles * parts && !(weights && sp.gt > 1)) {
@@ -1134,10 +1135,13 @@ Plan make_plan(int n_seq, int max_tokens, int heads, int kv_heads, int head_dim,
   return p;
 }
 
+// The limit on shared memory belongs to the kernel, not to the call: every call sets the most that
+// any call needs, so that one host thread's launch cannot meet a lower limit of another's.
 template <typename K>
 cudaError_t launch_attn(K kernel, int smem, const DecodeArgs& a, const Split& sp, cudaStream_t s) {
-  const int bytes = smem + sp.hpt * sp.held * (int)sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const int head_row = sp.hpt * (int)sizeof(float);            // (hpt: fixed by the kernel)
+  const int bytes = smem + head_row * sp.held, limit = smem + head_row * kHeldTiles * kTile;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
   if (e != cudaSuccess) return e;
   if (!sp.parts) return launch_dependent(kernel, (unsigned)(sp.slots * sp.hgroups), kThreads, bytes, s, a, sp);
   return launch_dependent_clusters(kernel, sp.parts, (unsigned)(a.c.n_seq * sp.hgroups * sp.parts), kThreads, bytes, s,
