@@ -523,7 +523,8 @@ SFM_API int sfm_paged_attention(const void* q, const void* k_pages, const void* 
  * accumulated weight, highest first (NaN last); ties by the lower slot.  The kept
  * rows at slots >= keep move, in ascending order, into the evicted slots < keep:
  * K, V, positions and weights; nothing else is touched, and slots >= keep hold
- * what they held.  lengths is not changed (each layer cuts at the same lengths);
+ * what they held.  A move from or to a slot on a page outside the pool is left out
+ * whole: the slot keeps what it has.  lengths is not changed (each layer cuts at the same lengths);
  * the new one is min(lengths[s], keep), and pages behind it are free.
  * SFM_EINVAL if keep < 1 or n_first + n_recent > keep.  workspace: max_tokens as for
  * sfm_paged_attention, cap included (may be NULL when it is 0).

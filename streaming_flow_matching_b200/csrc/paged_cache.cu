@@ -140,11 +140,15 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int item, const in
     int rt = -1, rf = -1;
     if (lane < kMoveRows && i0 + lane < n) {
       const int to = outs[i0 + lane], from = mvs[i0 + lane];
+      const size_t at = (size_t)item * a.cap;
+      const float w = a.weights[at + from];
+      const int pos = a.positions[at + from];
       rt = cache_row(a.c, seq, to, a.err);
       rf = cache_row(a.c, seq, from, a.err);
-      const size_t at = (size_t)item * a.cap;
-      a.weights[at + to] = a.weights[at + from];
-      a.positions[at + to] = a.positions[at + from];
+      if (rt >= 0 && rf >= 0) {                                // with a bad page on either side nothing moves
+        a.weights[at + to] = w;
+        a.positions[at + to] = pos;
+      }
     }
     for (int x0 = lane; x0 < kMoveRows * pieces; x0 += 128) {
       uint4 d[4];

@@ -55,3 +55,35 @@ def test_two_host_threads(cuda_device, dtype, d, h):
     assert codes == [{L.SFM_OK}, {L.SFM_OK}]
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
     assert L.check_call_error() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 32)])
+@pytest.mark.parametrize("n,keep,alone", [(64, 48, True), (1500, 700, False)])
+@pytest.mark.parametrize("where", ["from", "to", "both"])
+@pytest.mark.parametrize("bad", [-1, 10 ** 6])
+def test_evict_leaves_slots_on_a_bad_page_as_they_were(cuda_device, dtype, d, n, keep, alone, where, bad):
+    from streaming_flow_matching_b200 import paged_evict
+    hk, page = 2, 16
+    c = Cache([n], page, hk, d, dtype, seed=2)
+    assert (L.lib.sfm_paged_evict_workspace_bytes(1, n, hk, keep) == 0) == alone
+    w = torch.arange(n, device="cuda").float().expand(1, hk, n).contiguous()      # the last `keep` stay
+    pos = (torch.arange(n, device="cuda", dtype=torch.int32) + 5).expand(1, hk, n).contiguous()
+    at = c.rows(0, n)
+    dead = {"from": [(n - 3) // page], "to": [0], "both": [0, (n - 3) // page]}[where]
+    ek, ev, ew, ep = c.k.clone(), c.v.clone(), w.clone(), pos.clone()
+    moved = 0
+    for x in range(hk):
+        for a, b in zip(*R.evict(w[0, x].tolist(), pos[0, x].tolist(), n, keep, 0, 0)):
+            if a // page in dead or b // page in dead:
+                continue
+            moved += 1
+            for e, src in ((ek, c.k), (ev, c.v)):
+                e.view(-1, hk, d)[at[a], x] = src.view(-1, hk, d)[at[b], x]
+            ew[0, x, a], ep[0, x, a] = w[0, x, b], pos[0, x, b]
+    for i in dead:
+        c.table[0, i] = bad
+    paged_evict(c.k, c.v, c.table, ints([n]), w, pos, keep)
+    assert L.check_call_error() == 0x301
+    assert moved > 0 or n == 64
+    assert torch.equal(c.k, ek) and torch.equal(c.v, ev)
+    assert torch.equal(w, ew) and torch.equal(pos, ep)
