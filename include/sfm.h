@@ -482,7 +482,8 @@ SFM_API int sfm_attention_bounds(int n_q, int n_kv, const int* doc_starts, const
  * ([n_rows][n_kv_heads][D_h], K already rotated) go to its slots lengths[s] + i,
  * their positions become pos0[s] + i (pos0 NULL: lengths[s] + i) and their weights
  * 0.  row_starts: device int32 [n_seq + 1], ascending, or NULL: row s is sequence
- * s's (n_rows = n_seq).  Rows outside all ranges are ignored.  lengths is the
+ * s's (n_rows = n_seq).  Rows outside all ranges are ignored; a row whose slot is on a
+ * page outside the pool is dropped whole, its position and weight too.  lengths is the
  * count BEFORE the call and is not changed: every layer of a pass appends at the
  * same lengths.
  */

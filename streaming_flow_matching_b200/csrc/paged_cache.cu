@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     int seq, i;
     if (!place(r0 + rr, &seq, &i)) continue;
     const int t = slot_of(seq, i);
-    if (t < 0) continue;
+    if (t < 0 || cache_row(a.c, seq, t, nullptr) < 0) continue;    // the row was dropped (and recorded) above
     const size_t at = ((size_t)seq * hk + h) * a.cap + t;
     if (a.positions) a.positions[at] = (a.pos0 ? __ldg(a.pos0 + seq) : __ldg(a.c.lengths + seq)) + i;
     if (a.weights) a.weights[at] = 0.f;

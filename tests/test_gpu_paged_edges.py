@@ -87,3 +87,35 @@ def test_evict_leaves_slots_on_a_bad_page_as_they_were(cuda_device, dtype, d, n,
     assert moved > 0 or n == 64
     assert torch.equal(c.k, ek) and torch.equal(c.v, ev)
     assert torch.equal(w, ew) and torch.equal(pos, ep)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 96)])
+@pytest.mark.parametrize("bad", [-1, 10 ** 6])
+@pytest.mark.parametrize("pos0", [None, [7, 900]])
+def test_append_leaves_slots_on_a_bad_page_as_they_were(cuda_device, dtype, d, bad, pos0):
+    from streaming_flow_matching_b200 import paged_append
+    hk, page, cap = 3, 16, 100
+    c = Cache([60, 90], page, hk, d, dtype, seed=4)
+    before, rows = [5, 30], [55, 60]
+    starts = [0, 55, 115]
+    k, v = (torch.randn(115, hk, d, device="cuda").to(dtype) for _ in range(2))
+    w = torch.rand(2, hk, cap, device="cuda")
+    pos = torch.full((2, hk, cap), -7, dtype=torch.int32, device="cuda")
+    ek, ev, ew, ep = c.k.clone(), c.v.clone(), w.clone(), pos.clone()
+    dead = [(0, 1), (1, 3), (1, 4)]
+    for s in range(2):
+        at = c.rows(s, before[s] + rows[s])
+        for i in range(rows[s]):
+            t = before[s] + i
+            if (s, t // page) in dead:
+                continue
+            ek.view(-1, hk, d)[at[t]], ev.view(-1, hk, d)[at[t]] = k[starts[s] + i], v[starts[s] + i]
+            ew[s, :, t] = 0
+            ep[s, :, t] = (pos0 or before)[s] + i
+    for s, i in dead:
+        c.table[s, i] = bad
+    paged_append(k, v, c.k, c.v, c.table, ints(before), row_starts=ints(starts), positions=pos, weights=w,
+                 pos0=None if pos0 is None else ints(pos0))
+    assert L.check_call_error() == 0x301
+    assert torch.equal(c.k, ek) and torch.equal(c.v, ev)
+    assert torch.equal(w, ew) and torch.equal(pos, ep)
