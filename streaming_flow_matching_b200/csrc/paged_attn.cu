@@ -59,8 +59,8 @@ struct Split {
   int hpt;              // query heads per tile
   float* part;          // [slots][hgroups][2][hpt][D]
   float* ml;            // [slots][hgroups][2][hpt][2]: running max (log2), sum
-  float* lse;           // [n_seq][H] (log2; with weights)
-  float* scores;        // [n_seq][H][pitch] (log2; with weights)
+  float* lse;           // [n_seq][H] (log2, relative to the bias at Reach; with weights)
+  float* scores;        // [n_seq][H][pitch] (log2, without the bias; with weights)
   int pitch;            // max_tokens
   int joins;            // CTAs of the finishing kernel that join, before those that add weights
   int parts;            // CTAs of a (sequence, head group)'s cluster, 0: runs of tiles and a join
@@ -166,19 +166,82 @@ __device__ __forceinline__ float peer_float(const float* p, int rank) {
   return v;
 }
 
+// One score in log2 units, without the bias.
+template <bool CAP>
+__device__ __forceinline__ float scaled_score(float dot, float scale, float cap, float inv_cap) {
+  float s = dot * scale;
+  if (CAP) s = cap * tanhf(s * inv_cap);
+  return s * kLog2e;
+}
+
+// The bias.  A score with its bias is one number only where maxima are looked for: far from the
+// query it is as large as slope x distance (41,000 for 1/2 x 57,600: 2^-8 apart in fp32), and its
+// rounding would be the weights' error.  A weight takes score, bias and maximum apart, the product
+// unrounded: 2^(s + fma(-slope, distance, -m)), the sum small wherever the weight is not.  The
+// distance is taken in whole numbers first: a slope times an absolute position would lose what
+// tells neighbours apart.
+__device__ __forceinline__ float distance(int q_pos, int pos) { return fabsf((float)((long long)q_pos - pos)); }
+__device__ __forceinline__ float with_bias(float s, float slope2, float dist) { return fmaf(-slope2, dist, s); }
+__device__ __forceinline__ float weight_of(float s, float slope2, float dist, float m) {
+  return ex2_approx(s + fmaf(-slope2, dist, -m));
+}
+__device__ __forceinline__ int query_position(const DecodeArgs& a, int seq, int len) {
+  return a.q_positions ? __ldg(a.q_positions + seq) : len - 1;
+}
+
+// The least and the largest distance of a sequence's slots.  Its log-sum-exp goes to the finishing
+// kernel as one number and so relative to the bias there, at `at(slope)`, next to which it is small;
+// both kernels look for that distance themselves, all threads of a CTA.  red: a free place of shared
+// memory for 2 floats of each warp.  (Static shared memory would leave no room for a second CTA.)
+struct Reach {
+  float near, far;
+  __device__ float at(float slope2) const { return slope2 < 0.f ? far : near; }
+};
+template <int THREADS>
+__device__ Reach find_reach(const DecodeArgs& a, int seq, int hk, int n, float* red) {
+  if (!a.positions) return {0.f, (float)(n - 1)};
+  const int* ps = a.positions + ((size_t)seq * a.c.kv_heads + hk) * a.cap;
+  const int q_pos = query_position(a, seq, n), lane = threadIdx.x & 31;
+  float near = INFINITY, far = 0.f;
+#pragma unroll 8
+  for (int t = threadIdx.x; t < n; t += THREADS) {
+    const float d = distance(q_pos, __ldg(ps + t));
+    near = fminf(near, d);
+    far = fmaxf(far, d);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    near = fminf(near, __shfl_xor_sync(0xffffffffu, near, o));
+    far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, o));
+  }
+  if (lane == 0) {
+    red[threadIdx.x >> 5] = near;
+    red[THREADS / 32 + (threadIdx.x >> 5)] = far;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    near = fminf(near, red[w]);
+    far = fmaxf(far, red[THREADS / 32 + w]);
+  }
+  __syncthreads();                                             // the place is free again
+  return {near, far};
+}
+
 // The cluster's end: part_o [nh][D] and part_ml [nh][2] (max (log2), sum) hold this CTA's share of
 // heads h0, ...; its scores of `count` slots from tok0 on, if weights are wanted, are
 // scores[head * held + slot - tok0].
 constexpr int kMaxParts = 8, kMaxTileHeads = 16;
 constexpr int kHeldTiles = 2;                                   // tiles a CTA of a cluster has at most, with weights
 template <typename T, int D>
-__device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Split& sp, int seq, int part, int h0, int nh,
-                                               const float* part_o, float* part_ml, const float* scores, int tok0,
-                                               int count) {
+__device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Split& sp, int seq, int len, int part, int h0,
+                                               int nh, const float* part_o, float* part_ml, const float* scores,
+                                               int tok0, int count) {
   // (behind the partials, where the rings were: static shared memory would leave no room for a
   // second CTA on the SM)
   float (*share)[kMaxParts] = reinterpret_cast<float (*)[kMaxParts]>(part_ml + 2 * kMaxTileHeads);
-  float* lse = part_ml + (2 + kMaxParts) * kMaxTileHeads;
+  float* top = part_ml + (2 + kMaxParts) * kMaxTileHeads;      // of each head: maximum (-inf: no visible slot),
+  float* inv = top + kMaxTileHeads;                            // 1 / sum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   cluster_barrier(sp.parts);
   for (int hh = warp; hh < nh; hh += kWarps) {
@@ -194,7 +257,10 @@ __device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Split&
     for (int o = kMaxParts / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const bool have = sum > 0.f || sum != sum;
     if (in) share[hh][lane] = have ? f / sum : 0.f;
-    if (lane == 0) lse[hh] = mb + log2f(sum);
+    if (lane == 0) {
+      top[hh] = have ? mb : -INFINITY;
+      inv[hh] = 1.f / sum;
+    }
   }
   __syncthreads();
   for (int x = part * kThreads + threadIdx.x; x < nh * D; x += sp.parts * kThreads) {
@@ -207,11 +273,16 @@ __device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Split&
     reinterpret_cast<T*>(a.o)[((size_t)seq * a.heads + h0) * D + x] = (T)o;
   }
   if (scores) {
-    float* w = a.weights + ((size_t)seq * a.c.kv_heads + h0 / (a.heads / a.c.kv_heads)) * a.cap + tok0;
+    const size_t at = ((size_t)seq * a.c.kv_heads + h0 / (a.heads / a.c.kv_heads)) * a.cap + tok0;
+    float* w = a.weights + at;
+    const int q_pos = query_position(a, seq, len);
     for (int t = threadIdx.x; t < count; t += kThreads) {
+      const float dist = a.slopes ? distance(q_pos, a.positions ? __ldg(a.positions + at + t) : tok0 + t) : 0.f;
       float add = 0.f;
-      for (int hh = 0; hh < nh; ++hh)
-        if (lse[hh] != -INFINITY) add += ex2_approx(scores[hh * sp.held + t] - lse[hh]);
+      for (int hh = 0; hh < nh; ++hh) {
+        const float slope2 = a.slopes ? __ldg(a.slopes + h0 + hh) * kLog2e : 0.f;
+        if (top[hh] != -INFINITY) add += weight_of(scores[hh * sp.held + t], slope2, dist, top[hh]) * inv[hh];
+      }
       w[t] += add;
     }
   }
@@ -250,16 +321,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// One score in log2 units.  The distance is taken in whole numbers first: a slope times
-// an absolute position would lose what tells neighbours apart.
-template <bool CAP>
-__device__ __forceinline__ float finish_score(float dot, float scale, float cap, float inv_cap, float slope,
-                                              float dist) {
-  float s = dot * scale;
-  if (CAP) s = cap * tanhf(s * inv_cap);
-  return fmaf(-slope, dist, s) * kLog2e;
 }
 
 // Writes head `h` (of the tile, D values held one per thread tid < D) of a finished or
@@ -373,14 +434,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           m[nt][e] = -INFINITY;
           l[nt][e] = 0.f;
           const int hh = nt * 8 + 2 * t4 + e;
-          slope[nt][e] = BIAS && hh < nh ? __ldg(a.slopes + h0 + hh) : 0.f;
+          slope[nt][e] = BIAS && hh < nh ? __ldg(a.slopes + h0 + hh) * kLog2e : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
       }
-      if (BIAS) q_pos = a.q_positions ? __ldg(a.q_positions + cw.seq) : cw.len - 1;
+      if (BIAS) q_pos = query_position(a, cw.seq, cw.len);
       if (keep_scores)
         score_rows = CLUSTER ? own_scores + 2 * t4 * pitch - tok0
                              : sp.scores + ((size_t)cw.seq * a.heads + h0 + 2 * t4) * pitch;
@@ -427,18 +488,20 @@ __global__ void __launch_bounds__(kThreads, 2)
           p0 = in0 ? __ldg(ps + tok) : 0;
           p1 = in1 ? __ldg(ps + tok + 8) : 0;
         }
-        d0 = fabsf((float)((long long)q_pos - p0));
-        d1 = fabsf((float)((long long)q_pos - p1));
+        d0 = distance(q_pos, p0);
+        d1 = distance(q_pos, p1);
       }
+      auto biased = [&](int nt, int e) {
+        return BIAS ? with_bias(s[nt][e], slope[nt][e & 1], e < 2 ? d0 : d1) : s[nt][e];
+      };
       bool grow = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const bool in = e < 2 ? in0 : in1;
-          s[nt][e] = in ? finish_score<CAP>(s[nt][e], scale, a.softcap, inv_cap, slope[nt][e & 1], e < 2 ? d0 : d1)
-                        : -INFINITY;
-          grow |= s[nt][e] > m[nt][e & 1] + kGrow;            // also from m = -inf
+          s[nt][e] = in ? scaled_score<CAP>(s[nt][e], scale, a.softcap, inv_cap) : -INFINITY;
+          grow |= biased(nt, e) > m[nt][e & 1] + kGrow;       // also from m = -inf
         }
       if (keep_scores) {
         // raw scores for the pass that accumulates weights: 8 consecutive tokens per head
@@ -463,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(fmaxf(s[nt][e], s[nt][e + 2]), m[nt][e]);
+            float mx = fmaxf(fmaxf(biased(nt, e), biased(nt, e + 2)), m[nt][e]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             // nothing seen yet: the accumulators are zeros
@@ -484,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float mb = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-          p[e] = ex2_approx(s[nt][e] - mb);
+          p[e] = BIAS ? weight_of(s[nt][e], slope[nt][e & 1], e < 2 ? d0 : d1, mb) : ex2_approx(s[nt][e] - mb);
           l[nt][e & 1] += p[e];
         }
 #pragma unroll
@@ -515,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();                                             // the stage may be refilled
 #pragma unroll
     for (int i = 0; i + 1 < kStages; ++i) masks[i] = masks[i + 1];
-    const int seq = cw.seq;
+    const int seq = cw.seq, seq_len = cw.len;
     const bool seq_done = (cw.tile + 1) * kTile >= cw.len;
     if (it + 1 < n_tiles) cw.next(a.c);
     if ((CLUSTER || !seq_done) && it + 1 < n_tiles) continue;
@@ -525,6 +588,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     Segment sg{seg_start, !seq_done};
     float* obuf = reinterpret_cast<float*>(smem + kOffMerge);
     float* mlbuf = reinterpret_cast<float*>(smem + kOffMl);
+    Reach reach{0.f, 0.f};
+    if (BIAS && !CLUSTER && sp.lse && !sg.partial()) reach = find_reach<kThreads>(a, seq, hk, seq_len, mlbuf);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -574,7 +639,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         } else {
           reinterpret_cast<__nv_bfloat16*>(a.o)[((size_t)seq * a.heads + h0 + ht) * 128 + d] =
               __float2bfloat16(sum > 0.f || sum != sum ? o / sum : 0.f);
-          if (sp.lse && d == 0) sp.lse[(size_t)seq * a.heads + h0 + ht] = mb + log2f(sum);
+          if (sp.lse && d == 0) {
+            const float slope2 = BIAS ? __ldg(a.slopes + h0 + ht) * kLog2e : 0.f;
+            sp.lse[(size_t)seq * a.heads + h0 + ht] = fmaf(slope2, reach.at(slope2), mb) + log2f(sum);
+          }
         }
       }
       __syncthreads();
@@ -586,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       part_ml[2 * threadIdx.x] = -INFINITY;
       part_ml[2 * threadIdx.x + 1] = 0.f;
     }
-    cluster_finish<__nv_bfloat16, 128>(a, sp, own_seq, share.part, h0, nh, part_o, part_ml,
+    cluster_finish<__nv_bfloat16, 128>(a, sp, own_seq, own_len, share.part, h0, nh, part_o, part_ml,
                                        keep_scores ? own_scores : nullptr, tok0, min(own_len - tok0, n_tiles * kTile));
   }
 }
@@ -712,12 +780,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       m = -INFINITY;
       l = 0.f;
-      slope = a.slopes && my_head < nh ? __ldg(a.slopes + h0 + my_head) : 0.f;
+      slope = a.slopes && my_head < nh ? __ldg(a.slopes + h0 + my_head) * kLog2e : 0.f;
 #pragma unroll
       for (int hh = 0; hh < GT; ++hh)
 #pragma unroll
         for (int i = 0; i < DV; ++i) acc[hh][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      q_pos = a.q_positions ? __ldg(a.q_positions + cw.seq) : cw.len - 1;
+      q_pos = query_position(a, cw.seq, cw.len);
       __syncthreads();
     }
     const int sub = it % Ring::kSub;
@@ -763,14 +831,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       bool grow = false;
+      float dist[NO];
 #pragma unroll
       for (int e = 0; e < NO; ++e) {
         const int x = (my_step + e) * 4 + grp;                 // token of the stage
-        const float dist = fabsf((float)((long long)q_pos - pos[0][e]));
+        dist[e] = distance(q_pos, pos[0][e]);
         if (!((mk >> x) & 1u)) s[e] = -INFINITY;
-        else if (cap) s[e] = finish_score<true>(s[e], scale, a.softcap, inv_cap, slope, dist);
-        else s[e] = finish_score<false>(s[e], scale, 0.f, 0.f, slope, dist);
-        grow |= s[e] > m + kGrow;                              // also from m = -inf
+        else if (cap) s[e] = scaled_score<true>(s[e], scale, a.softcap, inv_cap);
+        else s[e] = scaled_score<false>(s[e], scale, 0.f, 0.f);
+        grow |= with_bias(s[e], slope, dist[e]) > m + kGrow;   // also from m = -inf
         if (keep_scores && my_head < nh && base + x < cw.len) {
           if (CLUSTER) own_scores[my_head * sp.held + base + x - tok0] = s[e];
           else sp.scores[((size_t)cw.seq * a.heads + h0 + my_head) * sp.pitch + base + x] = s[e];
@@ -779,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (__any_sync(0xffffffffu, grow)) {
         float mx = m;
 #pragma unroll
-        for (int e = 0; e < NO; ++e) mx = fmaxf(mx, s[e]);
+        for (int e = 0; e < NO; ++e) mx = fmaxf(mx, with_bias(s[e], slope, dist[e]));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1)
           if (o < LPH || o >= 8) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -801,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float mb = m == -INFINITY ? 0.f : m;
 #pragma unroll
       for (int e = 0; e < NO; ++e) {
-        s[e] = ex2_approx(s[e] - mb);
+        s[e] = weight_of(s[e], slope, dist[e], mb);
         l += s[e];
       }
 #pragma unroll
@@ -831,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int e = 0; e < NO; ++e) pos[i][e] = pos[i + 1][e];
     }
     if (sub + 1 < Ring::kSub) continue;
-    const int seq = cw.seq;
+    const int seq = cw.seq, seq_len = cw.len;
     const bool seq_done = (cw.tile + 1) * kTile >= cw.len;
     if (it + 1 < n_its) cw.next(a.c);
     if ((CLUSTER || !seq_done) && it + 1 < n_its) continue;
@@ -839,6 +908,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- the sequence, or the run, ends here: the warp's four groups, then the four warps
     fresh = true;
     Segment sg{seg_start, !seq_done};
+    Reach reach{0.f, 0.f};
+    if (!CLUSTER && a.slopes && sp.lse && !sg.partial()) reach = find_reach<kThreads>(a, seq, hk, seq_len, mlbuf);
     float sum = l * (1.f / DUP);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
@@ -890,7 +961,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       } else {
         reinterpret_cast<float*>(a.o)[((size_t)seq * a.heads + h0 + hh) * D + d] =
             sum > 0.f || sum != sum ? o / sum : 0.f;
-        if (sp.lse && d == 0) sp.lse[(size_t)seq * a.heads + h0 + hh] = mb + log2f(sum);
+        if (sp.lse && d == 0) {
+          const float slope2 = a.slopes ? __ldg(a.slopes + h0 + hh) * kLog2e : 0.f;
+          sp.lse[(size_t)seq * a.heads + h0 + hh] = fmaf(slope2, reach.at(slope2), mb) + log2f(sum);
+        }
       }
     }
     __syncthreads();
@@ -901,8 +975,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       part_ml[2 * threadIdx.x] = -INFINITY;
       part_ml[2 * threadIdx.x + 1] = 0.f;
     }
-    cluster_finish<float, D>(a, sp, own_seq, share.part, h0, nh, part_o, part_ml, keep_scores ? own_scores : nullptr,
-                             tok0, min(own_len - tok0, share.n_tiles * kTile));
+    cluster_finish<float, D>(a, sp, own_seq, own_len, share.part, h0, nh, part_o, part_ml,
+                             keep_scores ? own_scores : nullptr, tok0, min(own_len - tok0, share.n_tiles * kTile));
   }
 }
 
@@ -969,14 +1043,14 @@ constexpr int kTokThread = kAccTok / kFinThreads, kHeadsOnce = 4, kSumsOnce = 32
 // finished by one CTA is left alone, an empty one gets zeros; the partials are summed in a
 // fixed order (float4 column x run, runs strided over the CTA, then over its groups).  The
 // others add weights, one per (sequence, key head, kAccTok slots): weights += sum over the
-// key head's query heads of 2^(score - lse).  Only the part that does not depend on the
+// key head's query heads of 2^(score + bias - m) / l.  Only the part that does not depend on the
 // attention kernel runs before the wait for it.  (80 registers; 64 spill and are 2 to 15 % slower
 // with weights, a kernel of 47 for the joins alone 2 to 5 % where few sequences are joined.)
-template <typename T>
+template <typename T, bool BIAS>
 __global__ void __launch_bounds__(kFinThreads)
     paged_finish_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp, int blocks_per_item) {
   __shared__ float4 buf[kFinThreads];
-  __shared__ float sh[kSumsOnce];
+  __shared__ float4 sh[kSumsOnce];                             // maximum (-inf: no visible slot), 1 / sum, slope, Reach
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.heads / a.c.kv_heads;
   if ((int)blockIdx.x < sp.joins) {
@@ -1028,11 +1102,16 @@ __global__ void __launch_bounds__(kFinThreads)
   const Parts p = find_parts(a.c, sp, seq, lane);
   float* w = a.weights + (size_t)item * a.cap;
   float add[kTokThread];                                       // the slots' weights so far
+  float dist[kTokThread];
+  const int q_pos = BIAS ? query_position(a, seq, n) : 0;
 #pragma unroll
   for (int i = 0; i < kTokThread; ++i) {
     const int t = blk * kAccTok + i * kFinThreads + tid;
     add[i] = t < t1 ? w[t] : 0.f;
+    dist[i] = BIAS ? distance(q_pos, t < t1 && a.positions ? __ldg(a.positions + (size_t)item * a.cap + t) : t) : 0.f;
   }
+  Reach reach{0.f, 0.f};
+  if (BIAS && p.s0 == p.s1) reach = find_reach<kFinThreads>(a, seq, hk, n, reinterpret_cast<float*>(buf));
   grid_dependency_wait();
   const float* sc = sp.scores + ((size_t)seq * a.heads + hk * G) * sp.pitch + blk * kAccTok + tid;
   float step[kTokThread];
@@ -1053,23 +1132,26 @@ __global__ void __launch_bounds__(kFinThreads)
       if (g0) __syncthreads();
       for (int x = warp; x < kSumsOnce && g0 + x < G; x += kFinThreads / 32) {
         const int h = hk * G + g0 + x;
-        float m, l;
+        const float slope2 = BIAS ? __ldg(a.slopes + h) * kLog2e : 0.f;
+        float m, l = 1.f;
         if (p.s0 == p.s1) {                                    // the attention kernel left it whole
           m = __ldcg(sp.lse + (size_t)seq * a.heads + h);
         } else {
           join_ml(sp, G, h, p, lane, &m, &l);
-          m += log2f(l);
+          if (l == 0.f) m = -INFINITY;
         }
-        if (lane == 0) sh[x] = m;
+        if (lane == 0) sh[x] = make_float4(m, 1.f / l, slope2, reach.at(slope2));
       }
       __syncthreads();
     }
 #pragma unroll
     for (int x = 0; x < kHeadsOnce; ++x) {
-      const float ls = g0 + x < G ? sh[g0 % kSumsOnce + x] : -INFINITY;
-      if (ls == -INFINITY) continue;                           // no visible slot (every page bad)
+      if (g0 + x >= G) continue;
+      const float4 f = sh[g0 % kSumsOnce + x];
+      if (f.x == -INFINITY) continue;                          // no visible slot (every page bad)
 #pragma unroll
-      for (int i = 0; i < kTokThread; ++i) step[i] += ex2_approx(s[x][i] - ls);
+      for (int i = 0; i < kTokThread; ++i)
+        step[i] += (BIAS ? weight_of(s[x][i], f.z, dist[i] - f.w, f.x) : ex2_approx(s[x][i] - f.x)) * f.y;
     }
   }
 #pragma unroll
@@ -1195,7 +1277,10 @@ int launch_paged_attention(const DecodeArgs& a, int dtype, void* workspace, cuda
   ProfScope ps(SFM_PROF_ATTN_MERGE, s);
   const int per_item = (a.c.max_tokens + kAccTok - 1) / kAccTok;
   const unsigned fin = (unsigned)(sp.joins + (a.weights ? a.c.n_seq * a.c.kv_heads * per_item : 0));
-  auto kernel = dtype == SFM_DTYPE_BF16 ? paged_finish_kernel<__nv_bfloat16> : paged_finish_kernel<float>;
+  const bool bias = a.weights && a.slopes;                     // (the joins do not look at it)
+  auto kernel = dtype == SFM_DTYPE_BF16
+                    ? (bias ? paged_finish_kernel<__nv_bfloat16, true> : paged_finish_kernel<__nv_bfloat16, false>)
+                    : (bias ? paged_finish_kernel<float, true> : paged_finish_kernel<float, false>);
   return record_cuda(launch_dependent(kernel, fin, kFinThreads, 0, s, a, sp, per_item));
 }
 

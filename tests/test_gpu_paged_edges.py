@@ -119,3 +119,22 @@ def test_append_leaves_slots_on_a_bad_page_as_they_were(cuda_device, dtype, d, b
     assert L.check_call_error() == 0x301
     assert torch.equal(c.k, ek) and torch.equal(c.v, ev)
     assert torch.equal(w, ew) and torch.equal(pos, ep)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 32), (F32, 64), (F32, 96), (F32, 128)])
+@pytest.mark.parametrize("lens,h,hk", [([300, 64, 1], 6, 2), ([5000, 17, 3000], 8, 2), ([330] * 150 + [9, 0, 2000], 3, 1),
+                                       ([700], 20, 1)])
+@pytest.mark.parametrize("cap,sign", [(0.0, 1.0), (30.0, 1.0), (0.0, -1.0)])
+def test_attention_far_from_every_position(cuda_device, dtype, d, lens, h, hk, cap, sign):
+    n = max(lens)
+    c = Cache(lens, 16, hk, d, dtype, seed=len(lens) + h)
+    q = torch.randn(len(lens), h, d, device="cuda").to(dtype)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pos = torch.stack([torch.randperm(n + 5, generator=g, device="cuda") for _ in range(len(lens) * hk)])
+    pos = (pos.view(len(lens), hk, n + 5) * 3).to(torch.int32).contiguous()
+    for far in (57600, 1000003):
+        kw = dict(softcap=cap, slopes=sign * ladder(h), positions=pos, q_positions=ints([far + s for s in range(len(lens))]))
+        run(c, q, lens, weights=torch.rand(len(lens), hk, n + 5, device="cuda"), **kw)
+        run(c, q, lens, **kw)
+    kw["q_positions"] = ints([-9000] * len(lens))
+    run(c, q, lens, weights=torch.zeros(len(lens), hk, n + 5, device="cuda"), **kw)
