@@ -59,7 +59,7 @@ struct Split {
   int hpt;              // query heads per tile
   float* part;          // [slots][hgroups][2][hpt][D]
   float* ml;            // [slots][hgroups][2][hpt][2]: running max (log2), sum
-  float* lse;           // [n_seq][H] (log2, relative to the bias at Reach; with weights)
+  float* lse;           // [n_seq][H] (log2; with weights, of sequences finished by one CTA: see leave_sum)
   float* scores;        // [n_seq][H][pitch] (log2, without the bias; with weights)
   int pitch;            // max_tokens
   int joins;            // CTAs of the finishing kernel that join, before those that add weights
@@ -189,10 +189,9 @@ __device__ __forceinline__ int query_position(const DecodeArgs& a, int seq, int 
   return a.q_positions ? __ldg(a.q_positions + seq) : len - 1;
 }
 
-// The least and the largest distance of a sequence's slots.  Its log-sum-exp goes to the finishing
-// kernel as one number and so relative to the bias there, at `at(slope)`, next to which it is small;
-// both kernels look for that distance themselves, all threads of a CTA.  red: a free place of shared
-// memory for 2 floats of each warp.  (Static shared memory would leave no room for a second CTA.)
+// The least and the largest distance of a sequence's slots, looked for by all threads of a CTA.  red:
+// a free place of shared memory for 2 floats of each warp.  (Static shared memory would leave no room
+// for a second CTA.)
 struct Reach {
   float near, far;
   __device__ float at(float slope2) const { return slope2 < 0.f ? far : near; }
@@ -226,6 +225,25 @@ __device__ Reach find_reach(const DecodeArgs& a, int seq, int hk, int n, float* 
   }
   __syncthreads();                                             // the place is free again
   return {near, far};
+}
+// What the finishing kernel needs of a head of a sequence that one CTA finished: the maximum m and
+// the sum, two numbers with a bias, as it may be far larger than the logarithm of the sum.  The sum
+// is left behind the head's scores.  A sequence that fills its table has no place there: its
+// log-sum-exp is left as one number, relative to the bias at its nearest slot (the farthest of a
+// negative slope), next to which it is small, and both kernels look for that distance (some 6 us in
+// each; 300 sequences of 2,000 tokens, all full: 546 -> 603 us).
+__device__ __forceinline__ bool sum_behind(const Split& sp, int len) { return len < sp.pitch; }
+template <bool BIAS>
+__device__ __forceinline__ void leave_sum(const DecodeArgs& a, const Split& sp, int seq, int h, int len,
+                                          const Reach& reach, float m, float sum) {
+  const size_t row = (size_t)seq * a.heads + h;
+  if (BIAS && sum_behind(sp, len)) {
+    sp.lse[row] = sum == 0.f ? -INFINITY : m;
+    sp.scores[row * sp.pitch + len] = sum;
+    return;
+  }
+  const float slope2 = BIAS ? __ldg(a.slopes + h) * kLog2e : 0.f;
+  sp.lse[row] = fmaf(slope2, reach.at(slope2), m) + log2f(sum);
 }
 
 // The cluster's end: part_o [nh][D] and part_ml [nh][2] (max (log2), sum) hold this CTA's share of
@@ -589,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     float* obuf = reinterpret_cast<float*>(smem + kOffMerge);
     float* mlbuf = reinterpret_cast<float*>(smem + kOffMl);
     Reach reach{0.f, 0.f};
-    if (BIAS && !CLUSTER && sp.lse && !sg.partial()) reach = find_reach<kThreads>(a, seq, hk, seq_len, mlbuf);
+    if (BIAS && !CLUSTER && sp.lse && !sg.partial() && !sum_behind(sp, seq_len))
+      reach = find_reach<kThreads>(a, seq, hk, seq_len, mlbuf);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -639,10 +658,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         } else {
           reinterpret_cast<__nv_bfloat16*>(a.o)[((size_t)seq * a.heads + h0 + ht) * 128 + d] =
               __float2bfloat16(sum > 0.f || sum != sum ? o / sum : 0.f);
-          if (sp.lse && d == 0) {
-            const float slope2 = BIAS ? __ldg(a.slopes + h0 + ht) * kLog2e : 0.f;
-            sp.lse[(size_t)seq * a.heads + h0 + ht] = fmaf(slope2, reach.at(slope2), mb) + log2f(sum);
-          }
+          if (sp.lse && d == 0) leave_sum<BIAS>(a, sp, seq, h0 + ht, seq_len, reach, mb, sum);
         }
       }
       __syncthreads();
@@ -909,7 +925,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     fresh = true;
     Segment sg{seg_start, !seq_done};
     Reach reach{0.f, 0.f};
-    if (!CLUSTER && a.slopes && sp.lse && !sg.partial()) reach = find_reach<kThreads>(a, seq, hk, seq_len, mlbuf);
+    if (!CLUSTER && a.slopes && sp.lse && !sg.partial() && !sum_behind(sp, seq_len))
+      reach = find_reach<kThreads>(a, seq, hk, seq_len, mlbuf);
     float sum = l * (1.f / DUP);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
@@ -962,8 +979,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         reinterpret_cast<float*>(a.o)[((size_t)seq * a.heads + h0 + hh) * D + d] =
             sum > 0.f || sum != sum ? o / sum : 0.f;
         if (sp.lse && d == 0) {
-          const float slope2 = a.slopes ? __ldg(a.slopes + h0 + hh) * kLog2e : 0.f;
-          sp.lse[(size_t)seq * a.heads + h0 + hh] = fmaf(slope2, reach.at(slope2), mb) + log2f(sum);
+          if (a.slopes) leave_sum<true>(a, sp, seq, h0 + hh, seq_len, reach, mb, sum);
+          else leave_sum<false>(a, sp, seq, h0 + hh, seq_len, reach, mb, sum);
         }
       }
     }
@@ -1045,9 +1062,10 @@ constexpr int kTokThread = kAccTok / kFinThreads, kHeadsOnce = 4, kSumsOnce = 32
 // others add weights, one per (sequence, key head, kAccTok slots): weights += sum over the
 // key head's query heads of 2^(score + bias - m) / l.  Only the part that does not depend on the
 // attention kernel runs before the wait for it.  (80 registers; 64 spill and are 2 to 15 % slower
-// with weights, a kernel of 47 for the joins alone 2 to 5 % where few sequences are joined.)
+// with weights, 124, as the compiler would have them with a bias, 6 %, a kernel of 47 for the joins
+// alone 2 to 5 % where few sequences are joined.)
 template <typename T, bool BIAS>
-__global__ void __launch_bounds__(kFinThreads)
+__global__ void __launch_bounds__(kFinThreads, 3)
     paged_finish_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Split sp, int blocks_per_item) {
   __shared__ float4 buf[kFinThreads];
   __shared__ float4 sh[kSumsOnce];                             // maximum (-inf: no visible slot), 1 / sum, slope, Reach
@@ -1111,7 +1129,7 @@ __global__ void __launch_bounds__(kFinThreads)
     dist[i] = BIAS ? distance(q_pos, t < t1 && a.positions ? __ldg(a.positions + (size_t)item * a.cap + t) : t) : 0.f;
   }
   Reach reach{0.f, 0.f};
-  if (BIAS && p.s0 == p.s1) reach = find_reach<kFinThreads>(a, seq, hk, n, reinterpret_cast<float*>(buf));
+  if (BIAS && p.s0 == p.s1 && !sum_behind(sp, n)) reach = find_reach<kFinThreads>(a, seq, hk, n, reinterpret_cast<float*>(buf));
   grid_dependency_wait();
   const float* sc = sp.scores + ((size_t)seq * a.heads + hk * G) * sp.pitch + blk * kAccTok + tid;
   float step[kTokThread];
@@ -1136,6 +1154,7 @@ __global__ void __launch_bounds__(kFinThreads)
         float m, l = 1.f;
         if (p.s0 == p.s1) {                                    // the attention kernel left it whole
           m = __ldcg(sp.lse + (size_t)seq * a.heads + h);
+          if (BIAS && sum_behind(sp, n)) l = __ldcg(sp.scores + ((size_t)seq * a.heads + h) * sp.pitch + n);
         } else {
           join_ml(sp, G, h, p, lane, &m, &l);
           if (l == 0.f) m = -INFINITY;

@@ -138,3 +138,19 @@ def test_attention_far_from_every_position(cuda_device, dtype, d, lens, h, hk, c
         run(c, q, lens, **kw)
     kw["q_positions"] = ints([-9000] * len(lens))
     run(c, q, lens, weights=torch.zeros(len(lens), hk, n + 5, device="cuda"), **kw)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+@pytest.mark.parametrize("lens,h,hk", [([330] * 150, 3, 1), ([1300, 7, 1300, 0] * 40, 8, 2), ([70] * 200, 20, 1)])
+@pytest.mark.parametrize("cap,sign", [(0.0, 1.0), (30.0, -1.0)])
+def test_attention_far_with_full_tables(cuda_device, dtype, d, lens, h, hk, cap, sign):
+    # sequences as long as the state arrays, most of them finished by one CTA; ranks of positions and slots apart
+    n = max(lens)
+    c = Cache(lens, 16, hk, d, dtype, seed=len(lens))
+    q = torch.randn(len(lens), h, d, device="cuda").to(dtype)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    pos = torch.stack([torch.randperm(n, generator=g, device="cuda") for _ in range(len(lens) * hk)])
+    pos = (pos.view(len(lens), hk, n) * 40).to(torch.int32).contiguous()
+    for q_pos in (120000, -60000):
+        run(c, q, lens, softcap=cap, slopes=sign * ladder(h), positions=pos, q_positions=ints([q_pos] * len(lens)),
+            weights=torch.rand(len(lens), hk, n, device="cuda"))
