@@ -129,6 +129,15 @@ __device__ __forceinline__ void row_range(const MaskedArgs& m, int i, int* lo, i
   *hi = b;
 }
 
+// The distance of the key whose bias is the largest in a row's range: the nearest's, or with a
+// negative slope the farthest's.  A row's scores may be taken relative to the bias there: where all
+// its keys are far (slope 1/2, 57,600 keys away: 41,000 in log2 units, 2^-8 apart in fp32) they would
+// round away what tells the keys apart.
+__device__ __forceinline__ int bias_origin(int pos, int lo, int hi, float slope) {
+  if (slope < 0.f) return max(abs(pos - lo), abs(pos - (hi - 1)));
+  return pos < lo ? lo - pos : pos >= hi ? pos - (hi - 1) : 0;
+}
+
 // columns [lo, hi) of up to 32 as a bit mask
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
   lo = max(lo, 0);
@@ -1007,6 +1016,9 @@ __global__ void __launch_bounds__(FTHREADS)
   const bool cap = a.softcap > 0.f;
   const float inv_cap = cap ? 1.f / a.softcap : 0.f;
   const float slope = a.slopes ? __ldg(a.slopes + h) : 0.f;
+  int origin[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) origin[i] = bias_origin(a.n_kv - a.n_q + row0 + ty * 4 + i, lo[i], hi[i], slope);
   float m[4], l[4];
   F2 o[4][DV];
 #pragma unroll
@@ -1069,7 +1081,7 @@ __global__ void __launch_bounds__(FTHREADS)
         s2[i][c].get(&z0, &z);
         z = (z0 + z) * scale;
         if (cap) z = a.softcap * tanh_f32(z * inv_cap);
-        z = fmaf(-slope, fabsf((float)(pos - key)), z) * kLog2e;
+        z = fmaf(-slope, (float)(abs(pos - key) - origin[i]), z) * kLog2e;
         s[i][c] = key >= lo[i] && key < hi[i] ? z : -INFINITY;
         grow |= s[i][c] > m[i] + kRescaleLog2;                 // also from m = -inf
       }
