@@ -114,7 +114,7 @@ struct TcArgs {
   int qblocks;         // row blocks
   int n_splits;
   float* o_part;       // [split][n_q][H][D]
-  float* lse_part;     // [split][n_q][H] (log2)
+  float* lse_part;     // [split][n_q][H] (log2, relative to the row's bias at bias_origin)
   int* err;
   unsigned long long wait_ns;
   int fault;
@@ -849,8 +849,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                        : reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(m_.o) + at);
       for (int q = 0; q < D / (parts ? 4 : 8); ++q) d[q] = make_uint4(0u, 0u, 0u, 0u);
     }
-    if (lane < q_rows && parts)
-      args.lse_part[((size_t)split * m_.n_q + row_t + r) * m_.heads + h] = have ? m + log2f(l) : -INFINITY;
+    if (lane < q_rows && parts) {
+      // relative to the bias at its origin: m alone may be so large that the sum would round away
+      const float top = BIAS ? fmaf(sm.slope2, (float)bias_origin(my_pos, my_lo, my_hi, sm.slope2), m) : m;
+      args.lse_part[((size_t)split * m_.n_q + row_t + r) * m_.heads + h] = have ? top + log2f(l) : -INFINITY;
+    }
   }
 
   tc_fence_before();
