@@ -500,7 +500,8 @@ SFM_API int sfm_paged_append(const void* k, const void* v, void* k_pages, void* 
  *   o = sum_t softmax(s)_t v_t over slots t < lengths[s]   (length 0: zeros)
  *   weights[s][h_kv][t] += sum of softmax(s)_t over the query heads of h_kv
  * lengths counts the slots to attend to (the new token's own, once appended,
- * included).  o is a buffer other than q (SFM_EINVAL).  positions and q_positions
+ * included).  An infinity of V in use gives that infinity, or NaN where its weight is
+ * below 2^-126 (0 times infinity); a NaN gives NaN.  o is a buffer other than q (SFM_EINVAL).  positions and q_positions
  * go together; without slopes they are not read.  Any number of query heads per key
  * head.  Results do not depend on timing (partials are joined in a fixed order).
  * workspace: the size for max_tokens = max_pages * page_size, or cap where that is

@@ -274,7 +274,7 @@ __device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Split&
 #pragma unroll
     for (int o = kMaxParts / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const bool have = sum > 0.f || sum != sum;
-    if (in) share[hh][lane] = have ? f / sum : 0.f;
+    if (in) share[hh][lane] = l == 0.f ? -1.f : f / sum;       // (-1: no visible slot, maybe nothing written)
     if (lane == 0) {
       top[hh] = have ? mb : -INFINITY;
       inv[hh] = 1.f / sum;
@@ -285,8 +285,8 @@ __device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Split&
     float o = 0.f;
 #pragma unroll
     for (int r = 0; r < kMaxParts; ++r) {
-      const float f = r < sp.parts ? share[x / D][r] : 0.f;
-      if (f != 0.f) o = fmaf(f, peer_float(part_o + x, r), o);   // (0: that CTA may have written nothing)
+      const float f = r < sp.parts ? share[x / D][r] : -1.f;
+      if (!(f < 0.f)) o = fmaf(f, peer_float(part_o + x, r), o);   // (a share of 0 hides no infinity or NaN)
     }
     reinterpret_cast<T*>(a.o)[((size_t)seq * a.heads + h0) * D + x] = (T)o;
   }

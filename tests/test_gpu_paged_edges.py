@@ -154,3 +154,25 @@ def test_attention_far_with_full_tables(cuda_device, dtype, d, lens, h, hk, cap,
     for q_pos in (120000, -60000):
         run(c, q, lens, softcap=cap, slopes=sign * ladder(h), positions=pos, q_positions=ints([q_pos] * len(lens)),
             weights=torch.rand(len(lens), hk, n, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_a_weight_that_vanishes_hides_nothing(cuda_device, dtype, d, what):
+    # a non-finite element of V far away, in another CTA's share: the same in both forms
+    from streaming_flow_matching_b200 import paged_attention
+    lens = [500, 40]
+    c = Cache(lens, 16, 1, d, dtype, seed=9)
+    q = torch.randn(2, 2, d, device="cuda").to(dtype)
+    c.v.view(-1, 1, d)[c.rows(0, 500)[3], 0, 5] = float(what)
+    sl = torch.tensor([1.0, 0.5], device="cuda")              # 2^-717 and 2^-358 at the far end
+    wide = torch.cat([c.table, torch.full((2, 2500), -1, dtype=torch.int32, device="cuda")], 1)
+    code = L.SFM_DTYPE_BF16 if dtype == BF else L.SFM_DTYPE_FP32
+    need = L.lib.sfm_paged_attention_workspace_bytes
+    for t, big in ((c.table, False), (wide, True)):
+        assert (need(2, t.shape[1] * 16, 2, 1, d, code, 0) > 0) == big
+        out = paged_attention(q, c.k, c.v, t, ints(lens), slopes=sl)
+        assert not bool(torch.isfinite(out[0, :, 5]).any())
+        out[0, :, 5] = 0
+        assert bool(torch.isfinite(out).all())
+    assert L.check_call_error() == 0
