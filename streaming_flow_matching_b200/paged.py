@@ -48,6 +48,13 @@ def _dims(t, n, name, what):
     return shape
 
 
+def _i32(x, name):
+    """x, refused if a C int would take it for another number."""
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError(f"{name} must be a 32-bit number, got {x}")
+    return x
+
+
 def _scratch(workspace, need, dev):
     """(tensor to keep until the launch, pointer, bytes) of the caller's workspace or a new one."""
     if workspace is None:
@@ -162,6 +169,7 @@ def paged_evict(k_pages, v_pages, table, lengths, weights, positions, keep, *, n
     n_seq, width = _width(table)
     if weights is None or positions is None:
         raise ValueError("paged_evict needs weights and positions")
+    keep, n_first, n_recent = _i32(keep, "keep"), _i32(n_first, "n_first"), _i32(n_recent, "n_recent")
     cap, pos, wts = _capacity(positions, weights, n_seq, hk, dev)
     args = (_ptr(k_pages, dt, "k_pages", pool, dev), _ptr(v_pages, dt, "v_pages", pool, dev),
             _ptr(table, _I32, "table", (n_seq, width), dev), _ptr(lengths, _I32, "lengths", (n_seq,), dev))
@@ -178,6 +186,7 @@ def attention_bounds(n_q, n_kv, *, doc_starts=None, prefixes=None, causal=False,
     and its first prefixes[d].  Queries in no document get an empty range.
     """
     dev = _device()
+    n_q, n_kv = _i32(n_q, "n_q"), _i32(n_kv, "n_kv")
     n_docs = doc_starts.numel() - 1 if doc_starts is not None else (1 if prefixes is not None else 0)
     lo, hi = (_empty(n_q, dtype=_I32, device=dev), _empty(n_q, dtype=_I32, device=dev)) if out is None else out
     L.check(_bounds(

@@ -176,3 +176,21 @@ def test_a_weight_that_vanishes_hides_nothing(cuda_device, dtype, d, what):
         out[0, :, 5] = 0
         assert bool(torch.isfinite(out).all())
     assert L.check_call_error() == 0
+
+
+def test_numbers_past_32_bits_are_refused(cuda_device):
+    from streaming_flow_matching_b200 import attention_bounds, paged_evict
+    c = Cache([64], 16, 1, 128, BF)
+    w = torch.rand(1, 1, 64, device="cuda")
+    pos = torch.arange(64, device="cuda", dtype=torch.int32).view(1, 1, 64).contiguous()
+    ek, ew = c.k.clone(), w.clone()
+    for kw in (dict(keep=2 ** 32 + 8), dict(keep=8, n_first=2 ** 32), dict(keep=8, n_recent=2 ** 32 + 1), dict(keep=-2 ** 32 + 8),
+               dict(keep=2 ** 31)):
+        with pytest.raises(ValueError):
+            paged_evict(c.k, c.v, c.table, ints([64]), w, pos, **kw)
+    for n_q, n_kv in ((4, 2 ** 32 + 8), (4, 2 ** 31)):
+        with pytest.raises(ValueError):
+            attention_bounds(n_q, n_kv)
+    assert torch.equal(c.k, ek) and torch.equal(w, ew)
+    paged_evict(c.k, c.v, c.table, ints([64]), w, pos, 2 ** 31 - 1)      # longer than any sequence: nothing to do
+    assert torch.equal(c.k, ek) and torch.equal(w, ew)
