@@ -422,7 +422,7 @@ SFM_API int sfm_fm_solve_exact_velocity(const sfm_handle* h, const float* z0, fl
  *     infinity, or NaN where its weight is below 2^-126 (0 times infinity).
  *   - bf16 (D_h = 128): P is rounded to bf16 for the product with V, sums and
  *     statistics are fp32.  fp32 (D_h a multiple of 32, <= 128): fp32 throughout.
- *   - o is a buffer other than q, k, v (SFM_EINVAL if o == q).
+ *   - o is a buffer other than q, k, v (SFM_EINVAL if it starts where one of them does).
  *   - slopes need n_kv >= n_q (the queries sit at the last n_q keys' positions).
  *   - workspace: sfm_attention_masked_workspace_bytes(...) bytes, 16-byte aligned
  *     (may be NULL when that is 0); nothing in it has to be set, and calls that
@@ -442,6 +442,7 @@ SFM_API int sfm_attention_masked(const void* q, const void* k, const void* v, vo
  * n_kv - n_q + i and sees its own document: all of it, or (causal) the keys up
  * to its own and the document's first prefixes[d].  Queries before the first
  * document's start or behind the last one's end are padding: an empty range.
+ * key_lo and key_hi are two buffers (SFM_EINVAL if one).
  * doc_starts: device int32 [n_docs + 1], ascending (equal neighbours: an empty
  * document), or NULL for one document of all keys (then n_docs is 0, or 1 with
  * prefixes); prefixes: device int32 [n_docs] or NULL (0); key_lo, key_hi: device
@@ -483,7 +484,8 @@ SFM_API int sfm_attention_bounds(int n_q, int n_kv, const int* doc_starts, const
  * their positions become pos0[s] + i (pos0 NULL: lengths[s] + i) and their weights
  * 0.  row_starts: device int32 [n_seq + 1], ascending, or NULL: row s is sequence
  * s's (n_rows = n_seq).  Rows outside all ranges are ignored; a row whose slot is on a
- * page outside the pool is dropped whole, its position and weight too.  lengths is the
+ * page outside the pool is dropped whole, its position and weight too.  K and V need
+ * pools of their own (SFM_EINVAL if k_pages == v_pages).  lengths is the
  * count BEFORE the call and is not changed: every layer of a pass appends at the
  * same lengths.
  */

@@ -78,6 +78,7 @@ int sfm_paged_append(const void* k, const void* v, void* k_pages, void* v_pages,
   if (rc) return rc;
   const long long row_bytes = (long long)n_kv_heads * head_dim * elem_bytes(dtype);
   if (row_bytes > (1 << 24) || n_rows > INT_MAX - 256) return SFM_EUNSUPPORTED;
+  if (k_pages == v_pages) return SFM_EINVAL;        // K and V of a row would go to the same place
   Guard gd;
   if ((rc = call_guard(&gd))) return rc;
   a.k = k;
@@ -183,6 +184,7 @@ int sfm_attention_bounds(int n_q, int n_kv, const int* doc_starts, const int* pr
   if (n_docs < 0 || (doc_starts && n_docs < 1) || (!doc_starts && n_docs != (prefixes ? 1 : 0))) return SFM_EINVAL;
   if (!aligned(doc_starts, 4) || !aligned(prefixes, 4) || !aligned(key_lo, 4) || !aligned(key_hi, 4))
     return SFM_EINVAL;
+  if (key_lo == key_hi) return SFM_EINVAL;
   BoundsArgs a{n_q, n_kv, doc_starts, prefixes, n_docs, causal, key_lo, key_hi};
   return launch_attention_bounds(a, (cudaStream_t)stream);
 }
@@ -200,7 +202,7 @@ int sfm_attention_masked(const void* q, const void* k, const void* v, void* o, i
                          void* stream) {
   int rc = check_heads(n_heads, n_kv_heads, head_dim, dtype);
   if (rc) return rc;
-  if (!q || !k || !v || !o || o == q || n_q < 1 || n_kv < 1) return SFM_EINVAL;
+  if (!q || !k || !v || !o || o == q || o == k || o == v || n_q < 1 || n_kv < 1) return SFM_EINVAL;
   if (slopes && n_kv < n_q) return SFM_EINVAL;      // the bias needs the queries' positions among the keys
   if (!cap_ok(softcap)) return SFM_EINVAL;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(key_lo, 4) ||

@@ -142,3 +142,10 @@ def test_workspaces():
     assert mk(1, 40000, 8, 8, 128, BF) > 0
     assert mk(1, 40000, 8, 8, 64, F32) > 0 and mk(1, 64, 8, 8, 64, F32) == 0
     assert C.sizeof(C.c_size_t) == 8
+
+
+def test_one_buffer_for_two_results():
+    assert append() == L.SFM_EINVAL                           # (kp and vp are one by default here)
+    assert append(weights=None, positions=None, pos0=None) == L.SFM_EINVAL
+    assert masked(k=2 * P) == L.SFM_EINVAL and masked(v=2 * P) == L.SFM_EINVAL
+    assert L.lib.sfm_attention_bounds(4, 8, P, P, 2, 1, P, P, None) == L.SFM_EINVAL
