@@ -234,7 +234,8 @@ def bench_units(layers, cache_units, n_units, warmup, reps):
 
 def bench_paged(n_seq, tokens, heads, kv_heads, warmup, reps, page=64):
     """One decode step of n_seq sequences of `tokens` cached tokens: append, attention with
-    accumulated weights; and an eviction of a tenth of the cache."""
+    accumulated weights; and an eviction of a tenth of the cache, from the same weights and
+    positions each time (their copy back is timed on its own and taken off)."""
     g = torch.Generator(device="cuda").manual_seed(0)
     per = -(-(tokens + 1) // page)
     shape = (n_seq * per, page, kv_heads, 128)
@@ -251,7 +252,17 @@ def bench_paged(n_seq, tokens, heads, kv_heads, warmup, reps, page=64):
     t_att = _time(lambda: paged_attention(q, k, v, table, after), warmup, reps)
     t_wts = _time(lambda: paged_attention(q, k, v, table, after, weights=w), warmup, reps)
     keep = max(1, tokens - tokens // 10)
-    t_evi = _time(lambda: paged_evict(k, v, table, after, w, pos, keep), warmup, reps)
+    fresh = w.clone(), pos.clone()
+
+    def put_back():
+        w.copy_(fresh[0])
+        pos.copy_(fresh[1])
+
+    def put_back_and_evict():
+        put_back()
+        paged_evict(k, v, table, after, w, pos, keep)
+
+    t_evi = _time(put_back_and_evict, warmup, reps) - _time(put_back, warmup, reps)
     gbs = n_seq * (tokens + 1) * kv_heads * 512 / t_att / 1e6
     return {"case": "paged", "sequences": n_seq, "tokens": tokens, "heads": heads, "kv_heads": kv_heads,
             "append_ms": t_app, "attention_ms": t_att, "attention_weights_ms": t_wts, "evict_tenth_ms": t_evi,

@@ -194,3 +194,17 @@ def test_numbers_past_32_bits_are_refused(cuda_device):
     assert torch.equal(c.k, ek) and torch.equal(w, ew)
     paged_evict(c.k, c.v, c.table, ints([64]), w, pos, 2 ** 31 - 1)      # longer than any sequence: nothing to do
     assert torch.equal(c.k, ek) and torch.equal(w, ew)
+
+
+def test_eviction_is_timed_on_the_same_state(cuda_device, monkeypatch):
+    from streaming_flow_matching_b200 import microbench
+    seen, real = [], microbench.paged_evict
+
+    def spy(k, v, table, lengths, w, pos, keep, **kw):
+        seen.append((w.clone(), pos.clone()))
+        return real(k, v, table, lengths, w, pos, keep, **kw)
+
+    monkeypatch.setattr(microbench, "paged_evict", spy)
+    r = microbench.bench_paged(2, 300, 4, 2, 1, 3)
+    assert r["evict_tenth_ms"] > 0 and len(seen) >= 4
+    assert all(torch.equal(w, seen[0][0]) and torch.equal(p, seen[0][1]) for w, p in seen)
