@@ -25,7 +25,8 @@ _masked_bytes = lru_cache(4096)(L.lib.sfm_attention_masked_workspace_bytes)
 # of a few rows takes less time on the GPU than in here, so lookups are made once
 _append, _attention, _evict = L.lib.sfm_paged_append, L.lib.sfm_paged_attention, L.lib.sfm_paged_evict
 _bounds, _masked = L.lib.sfm_attention_bounds, L.lib.sfm_attention_masked
-_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+           or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 _device = torch.cuda.current_device
 _Tensor, _empty, _U8 = torch.Tensor, torch.empty, torch.uint8
 

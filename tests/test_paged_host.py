@@ -149,3 +149,19 @@ def test_one_buffer_for_two_results():
     assert append(weights=None, positions=None, pos0=None) == L.SFM_EINVAL
     assert masked(k=2 * P) == L.SFM_EINVAL and masked(v=2 * P) == L.SFM_EINVAL
     assert L.lib.sfm_attention_bounds(4, 8, P, P, 2, 1, P, P, None) == L.SFM_EINVAL
+
+
+def test_binding_without_the_raw_stream_call(monkeypatch):
+    # a torch that lacks it: the stream's handle comes by way of its Stream object
+    import importlib.util
+    import types
+
+    import torch
+
+    import streaming_flow_matching_b200.paged as paged
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: types.SimpleNamespace(cuda_stream=40 + dev))
+    spec = importlib.util.spec_from_file_location(paged.__name__ + "_again", paged.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    assert again._stream(2) == 42
