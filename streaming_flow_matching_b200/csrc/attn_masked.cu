@@ -65,24 +65,24 @@ __global__ void __launch_bounds__(256) attention_bounds_kernel(const __grid_cons
   int d = 0, start = 0, end = a.n_kv;
   bool in = true;
   if (a.doc_starts) {
-    in = pos >= __ldg(a.doc_starts) && pos < __ldg(a.doc_starts + a.n_docs);
+    in = pos >= load_late(a.doc_starts) && pos < load_late(a.doc_starts + a.n_docs);
     int x = 0, y = a.n_docs;                       // the last d with starts[d] <= pos
     while (in && y - x > 1) {
       const int mid = (x + y) >> 1;
-      if (__ldg(a.doc_starts + mid) <= pos) x = mid;
+      if (load_late(a.doc_starts + mid) <= pos) x = mid;
       else y = mid;
     }
     d = x;
     if (in) {
-      start = max(0, __ldg(a.doc_starts + d));
-      end = min(a.n_kv, __ldg(a.doc_starts + d + 1));
+      start = max(0, load_late(a.doc_starts + d));
+      end = min(a.n_kv, load_late(a.doc_starts + d + 1));
     }
   }
   if (in) {
     lo = start;
     hi = end;
     if (a.causal) {
-      const long long pre = (long long)start + (a.prefixes ? max(0, __ldg(a.prefixes + d)) : 0);
+      const long long pre = (long long)start + (a.prefixes ? max(0, load_late(a.prefixes + d)) : 0);
       hi = (int)min((long long)end, max((long long)pos + 1, pre));
     }
   }
@@ -122,8 +122,8 @@ struct TcArgs {
 
 // the key range of query row i, empty as [0, 0)
 __device__ __forceinline__ void row_range(const MaskedArgs& m, int i, int* lo, int* hi) {
-  int a = m.key_lo ? max(0, __ldg(m.key_lo + i)) : 0;
-  int b = m.key_hi ? min(m.n_kv, __ldg(m.key_hi + i)) : m.n_kv;
+  int a = m.key_lo ? max(0, load_late(m.key_lo + i)) : 0;
+  int b = m.key_hi ? min(m.n_kv, load_late(m.key_hi + i)) : m.n_kv;
   if (a >= b) a = b = 0;
   *lo = a;
   *hi = b;
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float scale = 0.08838834764831845f;                  // 1 / sqrt(128)
     sm.sc = CAP ? scale / m_.softcap : scale * kLog2e;
     sm.cap2 = m_.softcap * kLog2e;
-    sm.slope2 = BIAS ? __ldg(m_.slopes + h) * kLog2e : 0.f;
+    sm.slope2 = BIAS ? load_late(m_.slopes + h) * kLog2e : 0.f;
     sm.x_lim = CAP ? kTanhRange * m_.softcap / scale : 0.f;
     F2 poly[4];                                                // kTanhC in terms of x, times cap log2(e)
     if (CAP) {
@@ -869,8 +869,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 // dims idle).  A row no split of which saw a key gets zeros.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    masked_join_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_part,
-                       T* __restrict__ o, long long rows_heads, int dim, int n_splits) {
+    masked_join_kernel(const float* o_part, const float* lse_part,
+                       T* o, long long rows_heads, int dim, int n_splits) {
   grid_dependency_wait();
   const long long gw = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
@@ -964,8 +964,8 @@ constexpr int f32_smem() {
 // normalised partial and its log-sum-exp.
 template <int DV>
 __global__ void __launch_bounds__(FTHREADS)
-    attn_masked_f32_kernel(const __grid_constant__ MaskedArgs a, int n_splits, float* __restrict__ o_part,
-                           float* __restrict__ lse_part) {
+    attn_masked_f32_kernel(const __grid_constant__ MaskedArgs a, int n_splits, float* o_part,
+                           float* lse_part) {
   grid_dependency_wait();
   constexpr int DD = 32 * DV, P = DD + 4, SP = FN + 4;
   extern __shared__ __align__(16) float fsm[];
@@ -1018,7 +1018,7 @@ __global__ void __launch_bounds__(FTHREADS)
   const float scale = rsqrtf((float)DD);
   const bool cap = a.softcap > 0.f;
   const float inv_cap = cap ? 1.f / a.softcap : 0.f;
-  const float slope = a.slopes ? __ldg(a.slopes + h) : 0.f;
+  const float slope = a.slopes ? load_late(a.slopes + h) : 0.f;
   int origin[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) origin[i] = bias_origin(a.n_kv - a.n_q + row0 + ty * 4 + i, lo[i], hi[i], slope);

@@ -9,6 +9,14 @@
 namespace sfm {
 
 #ifdef __CUDACC__
+// How such a kernel reads what others may have written, inputs included: by plain loads, after the
+// wait.  The read-only path (__ldg, or const __restrict__ parameters) is open only to what nobody
+// writes while the kernel runs, and it runs from before its wait on: the compiler may move such a
+// load above the wait.
+template <typename T>
+__device__ __forceinline__ T load_late(const T* p) {
+  return *p;
+}
 // Waits until the grid this one depends on has completed and its writes are visible.
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");

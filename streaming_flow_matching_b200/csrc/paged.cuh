@@ -60,7 +60,7 @@ __device__ __forceinline__ int cache_len(const PagedCache& c, int s, int* err) {
 // table; -1 (recorded) if its page is not one of the pool's.
 __device__ __forceinline__ int cache_row(const PagedCache& c, int s, int t, int* err) {
   const int pg = (int)(((unsigned long long)(unsigned)t * c.magic) >> c.shift);
-  const int id = __ldg(c.table + (size_t)s * c.max_pages + pg);
+  const int id = load_late(c.table + (size_t)s * c.max_pages + pg);
   if ((unsigned)id >= (unsigned)c.n_pages) {
     record_err(err, kErrPage);
     return -1;

@@ -186,7 +186,7 @@ __device__ __forceinline__ float weight_of(float s, float slope2, float dist, fl
   return ex2_approx(s + fmaf(-slope2, dist, -m));
 }
 __device__ __forceinline__ int query_position(const DecodeArgs& a, int seq, int len) {
-  return a.q_positions ? __ldg(a.q_positions + seq) : len - 1;
+  return a.q_positions ? load_late(a.q_positions + seq) : len - 1;
 }
 
 // The least and the largest distance of a sequence's slots, looked for by all threads of a CTA.  red:
@@ -204,7 +204,7 @@ __device__ Reach find_reach(const DecodeArgs& a, int seq, int hk, int n, float* 
   float near = INFINITY, far = 0.f;
 #pragma unroll 8
   for (int t = threadIdx.x; t < n; t += THREADS) {
-    const float d = distance(q_pos, __ldg(ps + t));
+    const float d = distance(q_pos, load_late(ps + t));
     near = fminf(near, d);
     far = fmaxf(far, d);
   }
@@ -242,7 +242,7 @@ __device__ __forceinline__ void leave_sum(const DecodeArgs& a, const Split& sp, 
     sp.scores[row * sp.pitch + len] = sum;
     return;
   }
-  const float slope2 = BIAS ? __ldg(a.slopes + h) * kLog2e : 0.f;
+  const float slope2 = BIAS ? load_late(a.slopes + h) * kLog2e : 0.f;
   sp.lse[row] = fmaf(slope2, reach.at(slope2), m) + log2f(sum);
 }
 
@@ -295,10 +295,10 @@ __device__ __forceinline__ void cluster_finish(const DecodeArgs& a, const Split&
     float* w = a.weights + at;
     const int q_pos = query_position(a, seq, len);
     for (int t = threadIdx.x; t < count; t += kThreads) {
-      const float dist = a.slopes ? distance(q_pos, a.positions ? __ldg(a.positions + at + t) : tok0 + t) : 0.f;
+      const float dist = a.slopes ? distance(q_pos, a.positions ? load_late(a.positions + at + t) : tok0 + t) : 0.f;
       float add = 0.f;
       for (int hh = 0; hh < nh; ++hh) {
-        const float slope2 = a.slopes ? __ldg(a.slopes + h0 + hh) * kLog2e : 0.f;
+        const float slope2 = a.slopes ? load_late(a.slopes + h0 + hh) * kLog2e : 0.f;
         if (top[hh] != -INFINITY) add += weight_of(scores[hh * sp.held + t], slope2, dist, top[hh]) * inv[hh];
       }
       w[t] += add;
@@ -444,15 +444,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         const bool have = nt * 8 + g < nh;                    // heads past the group: zeros
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          qf[ks][nt][0] = have ? __ldg(q + (nt * 8 + g) * 64 + ks * 8 + t4) : 0u;
-          qf[ks][nt][1] = have ? __ldg(q + (nt * 8 + g) * 64 + ks * 8 + t4 + 4) : 0u;
+          qf[ks][nt][0] = have ? load_late(q + (nt * 8 + g) * 64 + ks * 8 + t4) : 0u;
+          qf[ks][nt][1] = have ? load_late(q + (nt * 8 + g) * 64 + ks * 8 + t4 + 4) : 0u;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           m[nt][e] = -INFINITY;
           l[nt][e] = 0.f;
           const int hh = nt * 8 + 2 * t4 + e;
-          slope[nt][e] = BIAS && hh < nh ? __ldg(a.slopes + h0 + hh) * kLog2e : 0.f;
+          slope[nt][e] = BIAS && hh < nh ? load_late(a.slopes + h0 + hh) * kLog2e : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -503,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         int p0 = tok, p1 = tok + 8;
         if (a.positions) {
           const int* ps = a.positions + ((size_t)cw.seq * a.c.kv_heads + hk) * a.cap;
-          p0 = in0 ? __ldg(ps + tok) : 0;
-          p1 = in1 ? __ldg(ps + tok + 8) : 0;
+          p0 = in0 ? load_late(ps + tok) : 0;
+          p1 = in1 ? load_late(ps + tok + 8) : 0;
         }
         d0 = distance(q_pos, p0);
         d1 = distance(q_pos, p1);
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int e = 0; e < NO; ++e) {
       at[e] = ld.tile * kTile + warp * kWarpTok + sub * TOK + (my_step + e) * 4 + grp;
       if (a.positions && at[e] < ld.len)
-        at[e] = __ldg(a.positions + ((size_t)ld.seq * a.c.kv_heads + hk) * a.cap + at[e]);
+        at[e] = load_late(a.positions + ((size_t)ld.seq * a.c.kv_heads + hk) * a.cap + at[e]);
     }
     const uint32_t dst = smem_u32(ring) + (uint32_t)(to_issue % DEPTH) * (2 * Ring::kHalf);
     *mask = (__ballot_sync(0xffffffffu, next_row >= 0) >> (sub * TOK)) & ((1u << TOK) - 1u);
@@ -791,12 +791,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int x = threadIdx.x; x < GT * (D / 4); x += kThreads) {
         const int hh = x / (D / 4), c = x - hh * (D / 4);
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (hh < nh) f = __ldg(reinterpret_cast<const float4*>(a.q) + ((size_t)cw.seq * a.heads + h0 + hh) * (D / 4) + c);
+        if (hh < nh) f = load_late(reinterpret_cast<const float4*>(a.q) + ((size_t)cw.seq * a.heads + h0 + hh) * (D / 4) + c);
         qs[x] = f;
       }
       m = -INFINITY;
       l = 0.f;
-      slope = a.slopes && my_head < nh ? __ldg(a.slopes + h0 + my_head) * kLog2e : 0.f;
+      slope = a.slopes && my_head < nh ? load_late(a.slopes + h0 + my_head) * kLog2e : 0.f;
 #pragma unroll
       for (int hh = 0; hh < GT; ++hh)
 #pragma unroll
@@ -1126,7 +1126,7 @@ __global__ void __launch_bounds__(kFinThreads, 3)
   for (int i = 0; i < kTokThread; ++i) {
     const int t = blk * kAccTok + i * kFinThreads + tid;
     add[i] = t < t1 ? w[t] : 0.f;
-    dist[i] = BIAS ? distance(q_pos, t < t1 && a.positions ? __ldg(a.positions + (size_t)item * a.cap + t) : t) : 0.f;
+    dist[i] = BIAS ? distance(q_pos, t < t1 && a.positions ? load_late(a.positions + (size_t)item * a.cap + t) : t) : 0.f;
   }
   Reach reach{0.f, 0.f};
   if (BIAS && p.s0 == p.s1 && !sum_behind(sp, n)) reach = find_reach<kFinThreads>(a, seq, hk, n, reinterpret_cast<float*>(buf));
@@ -1150,7 +1150,7 @@ __global__ void __launch_bounds__(kFinThreads, 3)
       if (g0) __syncthreads();
       for (int x = warp; x < kSumsOnce && g0 + x < G; x += kFinThreads / 32) {
         const int h = hk * G + g0 + x;
-        const float slope2 = BIAS ? __ldg(a.slopes + h) * kLog2e : 0.f;
+        const float slope2 = BIAS ? load_late(a.slopes + h) * kLog2e : 0.f;
         float m, l = 1.f;
         if (p.s0 == p.s1) {                                    // the attention kernel left it whole
           m = __ldcg(sp.lse + (size_t)seq * a.heads + h);

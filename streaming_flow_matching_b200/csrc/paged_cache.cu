@@ -47,18 +47,18 @@ __global__ void __launch_bounds__(kAppendThreads)
       return true;
     }
     int lo = 0, hi = a.c.n_seq;      // the last s with row_starts[s] <= r
-    if (r < __ldg(a.row_starts) || r >= __ldg(a.row_starts + hi)) return false;
+    if (r < load_late(a.row_starts) || r >= load_late(a.row_starts + hi)) return false;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(a.row_starts + mid) <= r) lo = mid;
+      if (load_late(a.row_starts + mid) <= r) lo = mid;
       else hi = mid;
     }
     *seq = lo;
-    *i = r - __ldg(a.row_starts + lo);
+    *i = r - load_late(a.row_starts + lo);
     return true;
   };
   auto slot_of = [&](int seq, int i) -> int {           // -1: outside the table (recorded)
-    const long long t = (long long)__ldg(a.c.lengths + seq) + i;
+    const long long t = (long long)load_late(a.c.lengths + seq) + i;
     if (t < i || t >= a.c.max_tokens) {
       record_err(a.err, kErrLength);
       return -1;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     const int t = slot_of(seq, i);
     if (t < 0 || cache_row(a.c, seq, t, nullptr) < 0) continue;    // the row was dropped (and recorded) above
     const size_t at = ((size_t)seq * hk + h) * a.cap + t;
-    if (a.positions) a.positions[at] = (a.pos0 ? __ldg(a.pos0 + seq) : __ldg(a.c.lengths + seq)) + i;
+    if (a.positions) a.positions[at] = (a.pos0 ? load_late(a.pos0 + seq) : load_late(a.c.lengths + seq)) + i;
     if (a.weights) a.weights[at] = 0.f;
   }
 }
@@ -209,7 +209,7 @@ __device__ __forceinline__ uint2 peer_words(const void* p, int rank) {          
 }
 
 template <bool HOLD>
-__device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict__ counts, int* __restrict__ lists,
+__device__ __forceinline__ void evict_select(const EvictArgs& a, int* counts, int* lists,
                                              int room, int item, int part_id, int parts, int from, int n,
                                              int fused_vecs, SelectShared& sh) {
   extern __shared__ unsigned ranks[];
@@ -225,7 +225,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
   for (int t0 = tid; t0 < n; t0 += kBatch * kSelThreads) {
     int p[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) p[u] = t0 + u * kSelThreads < n ? __ldg(pos + t0 + u * kSelThreads) : INT_MIN;
+    for (int u = 0; u < kBatch; ++u) p[u] = t0 + u * kSelThreads < n ? load_late(pos + t0 + u * kSelThreads) : INT_MIN;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) mx = max(mx, p[u]);
   }
@@ -239,7 +239,7 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
     mx = __reduce_max_sync(0xffffffffu, lane < parts ? (int)peer_word(&sh.total[0], lane) : INT_MIN);
   }
   const int recent_from = (int)max((long long)INT_MIN, (long long)mx - a.n_recent + 1);   // (n_recent > 0)
-  auto make_rank = [&](int t) { return rank_of(__ldg(w + t), __ldg(pos + t), a.n_first, a.n_recent > 0, recent_from); };
+  auto make_rank = [&](int t) { return rank_of(load_late(w + t), load_late(pos + t), a.n_first, a.n_recent > 0, recent_from); };
   auto rank = [&](int t) { return HOLD ? ranks[t] : make_rank(t); };
   // the keep-th largest rank, digit by digit: `want` of the ranks that match the
   // prefix found so far are still to be taken.  The first digit is counted as the
@@ -257,8 +257,8 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
           const int t = min(t0 + u * kSelThreads, n - 1);      // (a slot past the end: not used below)
-          wv[u] = __ldg(w + t);
-          pv[u] = __ldg(pos + t);
+          wv[u] = load_late(w + t);
+          pv[u] = load_late(pos + t);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -407,8 +407,8 @@ __device__ __forceinline__ void evict_select(const EvictArgs& a, int* __restrict
 }
 
 __global__ void __launch_bounds__(kSelThreads)
-    evict_select_kernel(const __grid_constant__ EvictArgs a, int* __restrict__ counts,
-                        int* __restrict__ lists, int room, int held, int parts, int fused_vecs) {
+    evict_select_kernel(const __grid_constant__ EvictArgs a, int* counts,
+                        int* lists, int room, int held, int parts, int fused_vecs) {
   __shared__ SelectShared sh;
   grid_dependency_wait();
   const int item = blockIdx.x / parts, part_id = blockIdx.x - item * parts;
@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(kSelThreads)
 }
 
 __global__ void __launch_bounds__(kMoveWarps * 32)
-    evict_move_kernel(const __grid_constant__ EvictArgs a, const int* __restrict__ counts,
-                      const int* __restrict__ lists, int room, int head_vecs, int blocks_per_item) {
+    evict_move_kernel(const __grid_constant__ EvictArgs a, const int* counts,
+                      const int* lists, int room, int head_vecs, int blocks_per_item) {
   grid_dependency_wait();
   const int item = blockIdx.x / blocks_per_item, blk = blockIdx.x - item * blocks_per_item;
   const int* outs = lists + (size_t)item * 2 * room;

@@ -165,3 +165,17 @@ def test_binding_without_the_raw_stream_call(monkeypatch):
     again = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(again)
     assert again._stream(2) == 42
+
+
+def test_dependent_kernels_read_by_plain_loads():
+    # a kernel that is set up while the one before still runs may not use the read-only path
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(L.__file__), "csrc")
+    users = [f for f in glob.glob(os.path.join(csrc, "*.cu*"))
+             if re.search(r"grid_dependency_wait|dependent\.cuh", open(f).read())]
+    assert {"paged_attn.cu", "paged_cache.cu", "attn_masked.cu", "paged.cuh"} <= {os.path.basename(f) for f in users}
+    for f in users:
+        code = re.sub(r"//[^\n]*", "", open(f).read())
+        assert not re.search(r"__ldg|__restrict__|ld\.global\.nc", code), f
