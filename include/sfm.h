@@ -424,6 +424,7 @@ SFM_API int sfm_fm_solve_exact_velocity(const sfm_handle* h, const float* z0, fl
  *     statistics are fp32.  fp32 (D_h a multiple of 32, <= 128): fp32 throughout.
  *   - o is a buffer other than q, k, v (SFM_EINVAL if it starts where one of them does).
  *   - slopes need n_kv >= n_q (the queries sit at the last n_q keys' positions).
+ *     Distances enter bf16 calls as fp32 numbers: above 2^24 (16.7 million) they round.
  *   - workspace: sfm_attention_masked_workspace_bytes(...) bytes, 16-byte aligned
  *     (may be NULL when that is 0); nothing in it has to be set, and calls that
  *     can overlap need their own.
@@ -502,7 +503,8 @@ SFM_API int sfm_paged_append(const void* k, const void* v, void* k_pages, void* 
  *   o = sum_t softmax(s)_t v_t over slots t < lengths[s]   (length 0: zeros)
  *   weights[s][h_kv][t] += sum of softmax(s)_t over the query heads of h_kv
  * lengths counts the slots to attend to (the new token's own, once appended,
- * included).  An infinity of V in use gives that infinity, or NaN where its weight is
+ * included).  Distances enter as fp32 numbers: above 2^24 (16.7 million) they round.
+ * An infinity of V in use gives that infinity, or NaN where its weight is
  * below 2^-126 (0 times infinity); a NaN gives NaN.  o is a buffer other than q (SFM_EINVAL).  positions and q_positions
  * go together; without slopes they are not read.  Any number of query heads per key
  * head.  Results do not depend on timing (partials are joined in a fixed order).

@@ -32,11 +32,11 @@
 //
 // Measured (bf16): a block's 256 rows over 128 keys take ~1.9 us in the steady state, 1.3
 // PFLOP/s, the softmax as long as the products beside it; set-up and output of a block 6 to 9
-// us.  8,192 packed causal queries of 24 heads, cap 50: 186 us (166 without the cap); 8,000 with
-// prefixes and a bias: 418 us (393 without); 48 queries over 2,148 keys: 17 us.
+// us.  8,192 packed causal queries of 24 heads, cap 50: 187 us (166 without the cap); 8,000 with
+// prefixes and a bias: 422 us (393 without); 48 queries over 2,148 keys: 17 us.
 //
 // fp32 runs on the CUDA cores in 32 x 64 tiles: 1,000 queries over 1,400 keys, 4 heads, D 64, in
-// documents 26 us; 1,000 over 6,000, 24 heads 1.29 ms, 28.6 TFLOP/s.
+// documents 26 us; 1,000 over 6,000, 24 heads 1.24 ms, 29.7 TFLOP/s.
 #include <limits.h>
 #include <math.h>
 
@@ -1211,9 +1211,10 @@ long long base_ctas(int n_q, int heads, int kv_heads) {
 // fp32 3.4) and, bf16, a CTA's set-up and output (7 us), in every wave of CTAs; the join (3.5 us,
 // and 2.5 of its 4 us of the host's time) and the partials (written and read, 4 TB/s).  bf16 runs
 // one CTA on an SM, so that splits also even out the last wave (924 queries over 57,600 keys, 24
-// heads, 96 CTAs: 900 us alone, 785 in three splits), if they gain a tenth by this count: the waves
-// read K and V again (1,200 queries, 120 CTAs: 1,012 us alone, 1,088 in six); fp32 runs four that
-// share it, and splits only fill the first.
+// heads, 96 CTAs: 900 us alone, 785 in three splits when the rule was made, 665 to 670 since), if they
+// gain a tenth by this count: the waves read K and V again (1,200 queries, 120 CTAs: 1,012 us alone,
+// 1,088 in six); fp32 runs several that share it (seven at D 32, four at 64, three at 96, two at 128;
+// the rule counts four), and splits only fill the first.
 // Against "at least two tiles a split (fp32: four), at most 16, within one wave": 1 query over
 // 2,148 keys, 1 head 12.9 -> 10.5 us, over 30,000 37 -> 25; 300 queries over themselves, 24 heads:
 // no splits either way.

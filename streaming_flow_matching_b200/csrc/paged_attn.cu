@@ -341,8 +341,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Writes head `h` (of the tile, D values held one per thread tid < D) of a finished or
-// partial sequence.  first: the run's first tile of the sequence is not its tile 0.
+// What a run holds of a sequence: earlier runs have tiles before, later ones tiles behind.  A run
+// has two places for partials: of the sequence that starts before it, and of the one that ends after.
 struct Segment {
   bool starts_before, ends_after;
   __device__ bool partial() const { return starts_before || ends_after; }

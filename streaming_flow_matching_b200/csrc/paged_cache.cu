@@ -11,7 +11,7 @@
 // does not depend on the order of its slots, so nothing is compacted: the kept rows
 // that lie at slots >= keep move into the evicted slots < keep, both in ascending
 // order, and no other row is touched.  Sources and destinations are disjoint, so
-// the moves run in any order.  Two kernels:
+// the moves run in any order.  Two kernels (one where few rows can move: select moves them):
 //   select  one CTA, or a cluster of 2 to 8, per (sequence, key head): the keep-th
 //           largest rank by radix selection (digits of 11, 11 and 10 bits, a histogram
 //           each), then the lists of evicted slots < keep and kept slots >= keep in slot
@@ -119,10 +119,6 @@ __device__ __forceinline__ int warp_sum(int v) {
   return v;
 }
 
-// lists: per (sequence, key head) `room` evicted slots then `room` moved slots; counts: one each.
-// The ranks are made once and kept in shared memory (`held` of them at most; a longer run of
-// slots makes them again in each of its passes).  Bound by instructions: a CTA passes over its
-// slots five times, so those passes over shared memory are kept short.
 // A warp moves kMoveRows rows at a time: their slots and pages are looked up by as many
 // lanes at once, then the 16-byte pieces of all of them (head_vecs of K and of V each) are
 // loaded four to a lane before the first is stored.
@@ -208,6 +204,10 @@ __device__ __forceinline__ uint2 peer_words(const void* p, int rank) {          
   return v;
 }
 
+// Ranks and lists.  lists: per (sequence, key head) `room` evicted slots then `room` moved slots;
+// counts: one each.  The ranks are made once and kept in shared memory (`held` of them at most; a
+// longer run of slots makes them again in each of its passes).  Bound by instructions: a CTA passes
+// over its slots five times, so those passes over shared memory are kept short.
 template <bool HOLD>
 __device__ __forceinline__ void evict_select(const EvictArgs& a, int* counts, int* lists,
                                              int room, int item, int part_id, int parts, int from, int n,
